@@ -51,6 +51,21 @@ SIGNATURES = {
                                       _vp, _c_float, _c_int, _vp, _c_size, _vp]),
     "diffattn_decode_noalloc": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _vp, _c_int, _c_int, _c_int, _vp,
                                          _c_float, _vp, _c_float, _vp]),
+    "diffattn_paged_step": (_c_int, [_vp, _vp, _c_int, _vp, _c_int, _vp, _c_int, _vp, _vp, _c_int, _c_int,
+                                     _vp, _vp, _vp, _vp, _vp, _vp]),
+    "diffattn_rope_table_scaled": (_c_int, [_c_int, _c_int, ctypes.c_double, _c_int, ctypes.c_double, _c_int,
+                                            ctypes.c_double, ctypes.c_double, _vp, _vp]),
+    "diffattn_rope": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
+                               _c_int, _vp, _vp, _vp]),
+    "diffattn_kv_append": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                    _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp]),
+    "diffattn_extend_plan_size": (_c_size, [_c_int] * 6),
+    "diffattn_extend_plan": (_c_int, [_vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _c_size,
+                                      _vp]),
+    "diffattn_extend_workspace_size": (_c_size, [_c_int] * 6),
+    "diffattn_extend": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _vp, _c_size, _c_int, _c_int, _c_int,
+                                 _c_int, _c_int, _c_int, _vp, _c_float, _vp, _c_float, _c_int, _vp, _vp, _c_size,
+                                 _vp]),
     "diffattn_device_status": (_c_int, [ctypes.POINTER(_c_int)]),
     "diffattn_set_wait_limit_ns": (_c_int, [_c_ll]),
     "diffattn_status_string": (ctypes.c_char_p, [_c_int]),

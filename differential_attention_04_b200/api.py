@@ -7,6 +7,7 @@ the functions return immediately (stream-ordered), like the C calls.
 from __future__ import annotations
 
 import ctypes
+from typing import NamedTuple
 
 import torch
 
@@ -16,6 +17,10 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_WORKSPACE, ERR_
 F32, BF16 = 0, 1
 # how the two maps are combined: softmax(S1) + c softmax(S2), c = -lambda, 0, +lambda
 MODE_DIFF, MODE_LAMBDA_ZERO, MODE_SUM = 0, 1, 2
+# which channels a rotation pairs: (2j, 2j + 1) or (j, j + rot / 2)
+ROPE_INTERLEAVED, ROPE_HALF = 0, 1
+# how a rotary table's frequencies are scaled
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
 
 
 class DiffAttnError(RuntimeError):
@@ -451,6 +456,195 @@ def diffattn_decode_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     _launch("diffattn_decode_noalloc", (q, k_cache, v_cache, cu_seqlens, lam, rms_w, out),
             _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(cu_seqlens), int(max_seqlen), _ptr(out), S, H, d,
             _ptr(lam), float(lambda_init), _ptr(rms_w), float(eps))
+    return out
+
+
+# ------------------------------------------------ serving from a paged cache --
+def _i32(name: str, t: torch.Tensor, *shape: int) -> None:
+    _need(t.dtype == torch.int32 and tuple(t.shape) == shape, f"{name} must be int32 of shape {shape}")
+
+
+def paged_step(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+               pool: torch.Tensor, page_size: int, num_tokens: int, pool_out: torch.Tensor | None = None, out=None):
+    """Block tables and slot maps of one step from the requests' lengths: (cu_q, kv_lens, positions, slots, info).
+
+    ctx_lens, new_lens: int32 [S] (new_lens -1: the request is finished); block_table: int32 [S, max_pages],
+    updated; free_pages: int32 ring of free pages, updated; pool: int32 [2] (head, count), replaced in place unless
+    pool_out is given; num_tokens: rows of positions and slots (-1 behind the last new token).  info: int32 [4]
+    (tokens, pages taken, pages returned, 0 or what is wrong; then the step took nothing)."""
+    _need(ctx_lens.dim() == 1 and block_table.dim() == 2 and free_pages.dim() == 1,
+          "ctx_lens must be [S], block_table [S, max_pages] and free_pages [ring_size]")
+    S, max_pages = block_table.shape
+    T = int(num_tokens)
+    _need(T >= 0, "num_tokens must not be negative")
+    _i32("ctx_lens", ctx_lens, S)
+    _i32("new_lens", new_lens, S)
+    _i32("block_table", block_table, S, max_pages)
+    _i32("free_pages", free_pages, free_pages.numel())
+    _i32("pool", pool, 2)
+    if pool_out is None:
+        pool_out = pool
+    _i32("pool_out", pool_out, 2)
+    if out is None:
+        new = lambda n: torch.empty(n, dtype=torch.int32, device=ctx_lens.device)
+        out = (new(S + 1), new(S), new(T), new(T), new(4))
+    _need(len(out) == 5, "out must hold (cu_q, kv_lens, positions, slots, info)")
+    cu_q, kv_lens, positions, slots, info = out
+    for name, t, n in (("cu_q", cu_q, S + 1), ("kv_lens", kv_lens, S), ("positions", positions, T),
+                       ("slots", slots, T), ("info", info, 4)):
+        _i32(name, t, n)
+    _launch("diffattn_paged_step", (ctx_lens, new_lens, block_table, free_pages, pool, pool_out, *out),
+            _ptr(ctx_lens), _ptr(new_lens), S, _ptr(block_table), max_pages, _ptr(free_pages), free_pages.numel(),
+            _ptr(pool), _ptr(pool_out), int(page_size), T, _ptr(cu_q), _ptr(kv_lens), _ptr(positions), _ptr(slots),
+            _ptr(info))
+    return cu_q, kv_lens, positions, slots, info
+
+
+def rope_table_scaled(N: int, rot: int, base: float = 10000.0, scaling: int = ROPE_PLAIN, factor: float = 1.0,
+                      orig_len: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                      device=None) -> torch.Tensor:
+    """(cos, sin) of n * theta'_j for n < N, j < rot/2 with the frequencies scaled for long contexts
+    (ROPE_LINEAR, ROPE_NTK, ROPE_YARN; the last also scales cos and sin): float32 [N, rot/2, 2]."""
+    t = torch.empty((N, rot // 2, 2), dtype=torch.float32, device=device or torch.device("cuda"))
+    _launch("diffattn_rope_table_scaled", (t,), int(N), int(rot), float(base), int(scaling), float(factor),
+            int(orig_len), float(beta_fast), float(beta_slow), _ptr(t))
+    return t
+
+
+def _rope_args(q, positions, table, T):
+    _need(table.dtype == torch.float32 and table.dim() == 3 and table.shape[2] == 2 and table.shape[0] >= 1 and
+          2 <= 2 * table.shape[1] <= q.shape[-1], "table must be float32 [n_pos, rot/2, 2] with rot <= d")
+    _need(positions.dtype == torch.int32 and positions.numel() == T, "positions must be int32 with one entry per row")
+    return table.shape[0], 2 * table.shape[1]
+
+
+def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table: torch.Tensor,
+         layout: int = ROPE_INTERLEAVED, inverse: bool = False, out=None):
+    """Queries and keys rotated at `positions`: (q', k').  q: [..., H, 2, d], k: [..., H_kv, 2, d] or None, float32
+    or bfloat16, with one position (int32) per row of the leading dimensions; table: rope_table or
+    rope_table_scaled, whose width says how many channels are rotated.  Rows with a negative position are left as
+    they are in `out` (which may be (q, k) itself).  ``inverse`` is the transposed map: gradients with respect to
+    q', k' go in, those with respect to q, k come out."""
+    _need(q.dim() >= 4 and q.shape[-2] == 2, "q must be [..., H, 2, d]")
+    H, d = q.shape[-3], q.shape[-1]
+    T = positions.numel()
+    _need(q.numel() == T * H * 2 * d, "positions must be int32 with one entry per row")
+    dt = BF16 if q.dtype == torch.bfloat16 else F32 if q.dtype == torch.float32 else None
+    _need(dt is not None, "dtype must be bfloat16 or float32")
+    H_kv = 0
+    if k is not None:
+        _need(k.dim() == q.dim() and k.shape[:-3] == q.shape[:-3] and tuple(k.shape[-2:]) == (2, d) and
+              k.dtype == q.dtype, "k must be [..., H_kv, 2, d] with q's rows and dtype")
+        H_kv = k.shape[-3]
+    n_pos, rot = _rope_args(q, positions, table, T)
+    if out is None:
+        out = (torch.empty_like(q), None if k is None else torch.empty_like(k))
+    _need(len(out) == 2, "out must hold (q', k')")
+    qo, ko = out
+    _like("q'", qo, q.shape, q.dtype)
+    _need((ko is None) == (k is None), "out must hold k' exactly when k is given")
+    ts = (q, positions, table, qo)
+    if k is not None:
+        _like("k'", ko, k.shape, k.dtype)
+        ts += (k, ko)
+    _launch("diffattn_rope", ts, _ptr(q), _ptr(k), _ptr(positions), _ptr(table), n_pos, T, H, H_kv, d, rot, dt,
+            int(layout), int(bool(inverse)), _ptr(qo), _ptr(ko))
+    return qo, ko
+
+
+def _cache_shapes(k_cache, v_cache, d, dtype):
+    """(num_pages, page_size, H_kv) of a paged cache."""
+    _need(k_cache.dim() == 5 and tuple(k_cache.shape[3:]) == (2, d) and k_cache.dtype == dtype,
+          "k_cache must be [num_pages, page_size, H_kv, 2, d] of q's dtype")
+    P, ps, H_kv = k_cache.shape[:3]
+    _like("v_cache", v_cache, (P, ps, H_kv, 2 * d), dtype)
+    return P, ps, H_kv
+
+
+def kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor | None, slots: torch.Tensor,
+              table: torch.Tensor | None, k_cache: torch.Tensor, v_cache: torch.Tensor,
+              layout: int = ROPE_INTERLEAVED, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The cache write of a step: returns q rotated at `positions`, and writes k rotated and v into the pages at
+    `slots` (int32 [T], page * page_size + offset; negative: nothing is written).  q: bfloat16 [T, H, 2, d];
+    k: [T, H_kv, 2, d]; v: [T, H_kv, 2d]; table None: no rotation."""
+    _need(q.dim() == 4 and q.shape[2] == 2 and q.dtype == torch.bfloat16, "q must be bfloat16 [T, H, 2, d]")
+    T, H, _, d = q.shape
+    num_pages, page_size, H_kv = _cache_shapes(k_cache, v_cache, d, torch.bfloat16)
+    _like("k", k, (T, H_kv, 2, d), torch.bfloat16)
+    _like("v", v, (T, H_kv, 2 * d), torch.bfloat16)
+    _i32("slots", slots, T)
+    n_pos = rot = 0
+    ts = (q, k, v, slots, k_cache, v_cache)
+    if table is not None:
+        _need(positions is not None, "positions must be int32 with one entry per row")
+        n_pos, rot = _rope_args(q, positions, table, T)
+        ts += (positions, table)
+    if out is None:
+        out = torch.empty_like(q)
+    _like("out", out, q.shape, q.dtype)
+    _launch("diffattn_kv_append", ts + (out,), _ptr(q), _ptr(k), _ptr(v),
+            None if table is None else _ptr(positions), _ptr(slots), _ptr(table), n_pos, T, H, H_kv, d, rot,
+            int(layout), num_pages, page_size, _ptr(out), _ptr(k_cache), _ptr(v_cache))
+    return out
+
+
+class ExtendPlan(NamedTuple):
+    """A step's schedule (extend_plan): the device buffer and the sizes it was made for."""
+    buf: torch.Tensor
+    S: int
+    T: int
+    H: int
+    H_kv: int
+    d: int
+    max_new: int
+
+
+def extend_plan(cu_q: torch.Tensor, kv_lens: torch.Tensor, num_tokens: int, H: int, H_kv: int, d: int, max_new: int,
+                causal: bool = True, buf: torch.Tensor | None = None) -> ExtendPlan:
+    """The schedule of a step's attention, made once and read by every layer.  cu_q: int32 [S + 1]; kv_lens: int32
+    [S]; num_tokens: rows of q; max_new: a host bound of the new tokens of a request."""
+    S = kv_lens.numel()
+    _i32("cu_q", cu_q, S + 1)
+    _i32("kv_lens", kv_lens, S)
+    n = (S, int(num_tokens), int(H), int(H_kv), int(d), int(max_new))
+    need = int(lib().diffattn_extend_plan_size(*n))
+    if buf is None:
+        buf = torch.empty(max(need, 16), dtype=torch.uint8, device=kv_lens.device)
+    _launch("diffattn_extend_plan", (cu_q, kv_lens, buf), _ptr(cu_q), _ptr(kv_lens), *n, int(bool(causal)), _ptr(buf),
+            buf.numel() * buf.element_size())
+    return ExtendPlan(buf, *n)
+
+
+def extend_workspace_size(plan: ExtendPlan) -> int:
+    return int(lib().diffattn_extend_workspace_size(*plan[1:]))
+
+
+def diffattn_extend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                    plan: ExtendPlan, lam: torch.Tensor, lambda_init: float, rms_w: torch.Tensor, eps: float = 1e-5,
+                    mode: int = MODE_DIFF, workspace: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+    """Differential attention of the step's new tokens over the paged cache.  q: bfloat16 [T, H, 2, d]; k_cache:
+    [num_pages, page_size, H_kv, 2, d]; v_cache: [num_pages, page_size, H_kv, 2d]; block_table: int32
+    [S, max_pages]; plan: extend_plan's.  Rows behind the last request are left as they are in `out`."""
+    _need(q.dim() == 4 and q.shape[2] == 2 and q.dtype == torch.bfloat16, "q must be bfloat16 [T, H, 2, d]")
+    T, H, _, d = q.shape
+    num_pages, page_size, H_kv = _cache_shapes(k_cache, v_cache, d, q.dtype)
+    _need((T, H, H_kv, d) == (plan.T, plan.H, plan.H_kv, plan.d), "the plan was made for other sizes")
+    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == plan.S,
+          "block_table must be int32 [S, max_pages] with the plan's S")
+    _scalar_f32("lam", lam)
+    _f32("rms_w", rms_w, 2 * d)
+    if out is None:
+        out = torch.zeros((T, H, 2 * d), dtype=q.dtype, device=q.device)
+    _like("out", out, (T, H, 2 * d), q.dtype)
+    need = extend_workspace_size(plan)
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    _launch("diffattn_extend", (q, k_cache, v_cache, block_table, plan.buf, lam, rms_w, workspace, out),
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1], num_pages, page_size,
+            _ptr(plan.buf), plan.buf.numel() * plan.buf.element_size(), plan.S, T, H, H_kv, d, plan.max_new,
+            _ptr(lam), float(lambda_init), _ptr(rms_w), float(eps), int(mode), _ptr(out), _ptr(workspace),
+            workspace.numel() * workspace.element_size())
     return out
 
 

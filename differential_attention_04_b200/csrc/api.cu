@@ -175,6 +175,8 @@ bool encode_4d_e2m1(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, 
   return encode_cached(m, MapKey{base, {d0, d1, d2, d3}, 4, 128});
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 bool fits_i32(long long x) { return x >= 0 && x < (1ll << 31); }
 
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
@@ -266,6 +268,32 @@ int bwd_tc_impl(const void* q, const void* k, const void* v, const void* dy, int
   return cuda_status(launch_bwd_sm100(m, dy, B, N, H, d, causal, lambda, lambda_init, rms_w, eps, mode, dq, dk, dv,
                                       dlambda, drms_w, workspace, saved, ctl, stream));
 }
+// What the paged calls share: head counts and widths.
+int check_heads(int T, int H, int H_kv, int d) {
+  if (T < 0 || H < 1 || H_kv < 1 || H % H_kv != 0 || d < 1) return DIFFATTN_ERR_INVALID_ARG;
+  return DIFFATTN_OK;
+}
+
+// The checks of diffattn_rope and diffattn_kv_append on the rotation.
+int check_rotation(int T, int H, int H_kv, int d, int rot, int layout, const void* positions, const float* table,
+                   int n_pos) {
+  if (T < 0 || H < 1 || H_kv < 0 || d < 1 || rot < 2 || rot > d || rot % 2) return DIFFATTN_ERR_INVALID_ARG;
+  if (layout != DIFFATTN_ROPE_INTERLEAVED && layout != DIFFATTN_ROPE_HALF) return DIFFATTN_ERR_INVALID_ARG;
+  if (!positions || !table || n_pos < 1) return DIFFATTN_ERR_INVALID_ARG;
+  if (!aligned16(table) || !aligned4(positions)) return DIFFATTN_ERR_INVALID_ARG;
+  if (d % 8 || d > 256) return DIFFATTN_ERR_UNSUPPORTED;
+  return DIFFATTN_OK;
+}
+
+int check_extend_shape(const ExtendShape& n) {
+  if (n.S < 1 || n.max_new < 0) return DIFFATTN_ERR_INVALID_ARG;
+  const int st = check_heads(n.T, n.H, n.H_kv, n.d);
+  if (st != DIFFATTN_OK) return st;
+  if (!fits_i32(static_cast<long long>(n.T) * n.H * 2 * n.d)) return DIFFATTN_ERR_INVALID_ARG;
+  if (n.d != 64 && n.d != 128) return DIFFATTN_ERR_UNSUPPORTED;
+  if (n.S > 65535 || n.H > 65535 || n.H / n.H_kv > 128) return DIFFATTN_ERR_UNSUPPORTED;
+  return DIFFATTN_OK;
+}
 }  // namespace
 
 int* status_word() {
@@ -304,7 +332,8 @@ using namespace diffattn;
 
 extern "C" {
 
-int diffattn_version(void) { return 101; }  // 1.01: adds diffattn_quantize_qk4 and diffattn_fwd_qk4
+// 1.01: adds diffattn_quantize_qk4 and diffattn_fwd_qk4; 1.02: the paged serving calls
+int diffattn_version(void) { return 102; }
 
 const char* diffattn_status_string(int s) {
   switch (s) {
@@ -563,6 +592,174 @@ int diffattn_decode_mode(const void* q, const void* k_cache, const void* v_cache
   if (!workspace || ws_bytes < need || !aligned16(workspace)) return DIFFATTN_ERR_WORKSPACE;
   return cuda_status(launch_decode(q, k_cache, v_cache, cu_seqlens, max_seqlen, o, S, H, d, lambda, lambda_init,
                                    rms_w, eps, mode, workspace, stream));
+}
+
+int diffattn_rope_table_scaled(int seq_len, int rot, double base, int scaling, double factor, int orig_len,
+                               double beta_fast, double beta_slow, float* table, cudaStream_t stream) {
+  if (seq_len < 1 || rot < 2 || rot % 2 || !(base > 0.0) || !table || !aligned16(table))
+    return DIFFATTN_ERR_INVALID_ARG;
+  if (scaling < DIFFATTN_ROPE_PLAIN || scaling > DIFFATTN_ROPE_YARN) return DIFFATTN_ERR_INVALID_ARG;
+  if (scaling != DIFFATTN_ROPE_PLAIN && !(factor >= 1.0 && factor <= 1e6)) return DIFFATTN_ERR_INVALID_ARG;
+  if (scaling == DIFFATTN_ROPE_NTK && rot == 2) return DIFFATTN_ERR_INVALID_ARG;
+  if (scaling == DIFFATTN_ROPE_YARN && (orig_len < 1 || !(beta_slow >= 0.0) || !(beta_fast > beta_slow)))
+    return DIFFATTN_ERR_INVALID_ARG;
+  if (!fits_i32(static_cast<long long>(seq_len) * rot)) return DIFFATTN_ERR_INVALID_ARG;
+  return cuda_status(launch_rope_table_scaled(seq_len, rot, base, scaling, factor, orig_len, beta_fast, beta_slow,
+                                              table, stream));
+}
+
+int diffattn_rope(const void* q, const void* k, const int* positions, const float* table, int n_pos, int T, int H,
+                  int H_kv, int d, int rot, int dtype, int layout, int inverse, void* q_out, void* k_out,
+                  cudaStream_t stream) {
+  if (dtype != DIFFATTN_F32 && dtype != DIFFATTN_BF16) return DIFFATTN_ERR_INVALID_ARG;
+  if (T == 0 && H >= 1) return DIFFATTN_OK;
+  const int st = check_rotation(T, H, H_kv, d, rot, layout, positions, table, n_pos);
+  if (st != DIFFATTN_OK) return st;
+  if (!q || !q_out || (H_kv > 0 && (!k || !k_out))) return DIFFATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(k_out)) return DIFFATTN_ERR_INVALID_ARG;
+  if (!fits_i32(static_cast<long long>(T) * 2 * (H + H_kv) * d) || !fits_i32(static_cast<long long>(n_pos) * rot))
+    return DIFFATTN_ERR_INVALID_ARG;
+  RopeParams p = {};
+  p.q = q;
+  p.k = k;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.positions = positions;
+  p.table = table;
+  p.n_pos = n_pos;
+  p.T = T;
+  p.H = H;
+  p.H_kv = H_kv;
+  p.d = d;
+  p.rot = rot;
+  p.inverse = inverse ? 1 : 0;
+  if (status_ptr(&p.status) != cudaSuccess) return DIFFATTN_ERR_CUDA;
+  return cuda_status(launch_rope_rows(p, dtype == DIFFATTN_BF16, layout, stream));
+}
+
+int diffattn_kv_append(const void* q, const void* k, const void* v, const int* positions, const int* slots,
+                       const float* table, int n_pos, int T, int H, int H_kv, int d, int rot, int layout,
+                       int num_pages, int page_size, void* q_out, void* k_cache, void* v_cache, cudaStream_t stream) {
+  if (T == 0 && H >= 1 && H_kv >= 1) return DIFFATTN_OK;
+  if (H_kv < 1 || num_pages < 1 || page_size < 1) return DIFFATTN_ERR_INVALID_ARG;
+  // without a table nothing is rotated and positions, n_pos, rot and layout are not read
+  if (table) {
+    const int st = check_rotation(T, H, H_kv, d, rot, layout, positions, table, n_pos);
+    if (st != DIFFATTN_OK) return st;
+  } else {
+    rot = 8;
+    n_pos = 1;
+    layout = DIFFATTN_ROPE_INTERLEAVED;
+    if (T < 0 || H < 1 || d < 1) return DIFFATTN_ERR_INVALID_ARG;
+    if (d % 8 || d > 256) return DIFFATTN_ERR_UNSUPPORTED;
+  }
+  if (!q || !k || !v || !slots || !q_out || !k_cache || !v_cache || !aligned4(slots)) return DIFFATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_cache) ||
+      !aligned16(v_cache))
+    return DIFFATTN_ERR_INVALID_ARG;
+  if (!fits_i32(static_cast<long long>(T) * 2 * (H + H_kv) * d) || !fits_i32(static_cast<long long>(n_pos) * rot) ||
+      !fits_i32(static_cast<long long>(num_pages) * page_size))
+    return DIFFATTN_ERR_INVALID_ARG;
+  RopeParams p = {};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_out = q_out;
+  p.k_out = k_cache;
+  p.v_out = v_cache;
+  p.positions = positions;
+  p.slots = slots;
+  p.table = table;
+  p.n_pos = n_pos;
+  p.T = T;
+  p.H = H;
+  p.H_kv = H_kv;
+  p.d = d;
+  p.rot = rot;
+  p.num_slots = num_pages * page_size;
+  if (status_ptr(&p.status) != cudaSuccess) return DIFFATTN_ERR_CUDA;
+  return cuda_status(launch_rope_rows(p, 1, layout, stream));
+}
+
+int diffattn_paged_step(const int* ctx_lens, const int* new_lens, int S, int* block_table, int max_pages,
+                        int* free_pages, int ring_size, const int* pool, int* pool_out, int page_size, int T,
+                        int* cu_q, int* kv_lens, int* positions, int* slots, int* info, cudaStream_t stream) {
+  if (S < 1 || max_pages < 1 || ring_size < 1 || page_size < 1 || T < 0) return DIFFATTN_ERR_INVALID_ARG;
+  if (!ctx_lens || !new_lens || !block_table || !free_pages || !pool || !pool_out || !cu_q || !kv_lens || !info)
+    return DIFFATTN_ERR_INVALID_ARG;
+  if (T > 0 && (!positions || !slots)) return DIFFATTN_ERR_INVALID_ARG;
+  for (const void* a : {static_cast<const void*>(ctx_lens), static_cast<const void*>(new_lens),
+                        static_cast<const void*>(block_table), static_cast<const void*>(free_pages),
+                        static_cast<const void*>(pool), static_cast<const void*>(pool_out),
+                        static_cast<const void*>(cu_q), static_cast<const void*>(kv_lens),
+                        static_cast<const void*>(positions), static_cast<const void*>(slots),
+                        static_cast<const void*>(info)})
+    if (!aligned4(a)) return DIFFATTN_ERR_INVALID_ARG;
+  if (S > kPagedStepMaxRequests) return DIFFATTN_ERR_UNSUPPORTED;
+  return cuda_status(launch_paged_step(ctx_lens, new_lens, S, block_table, max_pages, free_pages, ring_size, pool,
+                                       pool_out, page_size, T, cu_q, kv_lens, positions, slots, info, stream));
+}
+
+size_t diffattn_extend_plan_size(int S, int T, int H, int H_kv, int d, int max_new) {
+  const ExtendShape n = {S, T, H, H_kv, d, max_new};
+  return check_extend_shape(n) == DIFFATTN_OK ? extend_plan_bytes(n) : 0;
+}
+
+size_t diffattn_extend_workspace_size(int S, int T, int H, int H_kv, int d, int max_new) {
+  const ExtendShape n = {S, T, H, H_kv, d, max_new};
+  return check_extend_shape(n) == DIFFATTN_OK ? extend_workspace_bytes(n) : 0;
+}
+
+int diffattn_extend_plan(const int* cu_q, const int* kv_lens, int S, int T, int H, int H_kv, int d, int max_new,
+                         int causal, void* plan, size_t plan_bytes, cudaStream_t stream) {
+  const ExtendShape n = {S, T, H, H_kv, d, max_new};
+  const int st = check_extend_shape(n);
+  if (st != DIFFATTN_OK) return st;
+  if (!cu_q || !kv_lens || !aligned4(cu_q) || !aligned4(kv_lens)) return DIFFATTN_ERR_INVALID_ARG;
+  if (!plan || plan_bytes < extend_plan_bytes(n) || !aligned16(plan)) return DIFFATTN_ERR_WORKSPACE;
+  DevCtl ctl;
+  if (dev_ctl(&ctl) != cudaSuccess) return DIFFATTN_ERR_CUDA;
+  return cuda_status(launch_extend_plan(cu_q, kv_lens, n, causal, plan, ctl, stream));
+}
+
+int diffattn_extend(const void* q, const void* k_cache, const void* v_cache, const int* block_table, int max_pages,
+                    int num_pages, int page_size, const void* plan, size_t plan_bytes, int S, int T, int H, int H_kv,
+                    int d, int max_new, const float* lambda, float lambda_init, const float* rms_w, float eps,
+                    int mode, void* o, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  ExtendArgs a = {};
+  a.n = ExtendShape{S, T, H, H_kv, d, max_new};
+  const int st = check_extend_shape(a.n);
+  if (st != DIFFATTN_OK) return st;
+  if (max_pages < 1 || num_pages < 1 || page_size < 1 || !(eps >= 0.f)) return DIFFATTN_ERR_INVALID_ARG;
+  if (mode != DIFFATTN_MODE_DIFF && mode != DIFFATTN_MODE_LAMBDA_ZERO && mode != DIFFATTN_MODE_SUM)
+    return DIFFATTN_ERR_INVALID_ARG;
+  if (!fits_i32(static_cast<long long>(num_pages) * page_size)) return DIFFATTN_ERR_INVALID_ARG;
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return DIFFATTN_ERR_UNSUPPORTED;
+  if (T == 0 || max_new == 0) return DIFFATTN_OK;
+  if (!q || !k_cache || !v_cache || !block_table || !o || !lambda || !rms_w) return DIFFATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned4(block_table))
+    return DIFFATTN_ERR_INVALID_ARG;
+  if (!plan || plan_bytes < extend_plan_bytes(a.n) || !aligned16(plan)) return DIFFATTN_ERR_WORKSPACE;
+  const size_t need = extend_workspace_bytes(a.n);
+  if (need > 0 && (!workspace || ws_bytes < need || !aligned16(workspace))) return DIFFATTN_ERR_WORKSPACE;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.block_table = block_table;
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.plan = plan;
+  a.lambda = lambda;
+  a.lambda_init = lambda_init;
+  a.rms_w = rms_w;
+  a.eps = eps;
+  a.mode = mode;
+  a.o = o;
+  a.workspace = workspace;
+  DevCtl ctl;
+  if (dev_ctl(&ctl) != cudaSuccess) return DIFFATTN_ERR_CUDA;
+  return cuda_status(launch_extend(a, ctl, stream));
 }
 
 }  // extern "C"

@@ -136,4 +136,50 @@ cudaError_t launch_decode(const void* q, const void* k_cache, const void* v_cach
                           int max_seqlen, void* o, int S, int H, int d, const float* lambda, float lambda_init,
                           const float* rms_w, float eps, int mode, void* workspace, cudaStream_t stream);
 
+// Rotary positions at given rows (rope.cu).  Rows of q are [T][2 H][d], of k
+// [T][2 H_kv][d], of v (cache write only, else null) [T][H_kv][2d]; with slots
+// non-null k_out and v_out are caches of num_slots rows, else k_out has T.
+struct RopeParams {
+  const void *q, *k, *v;
+  void *q_out, *k_out, *v_out;
+  const int *positions, *slots;
+  const float* table;  // [n_pos][rot / 2] (cos, sin); null: no rotation (cache write only)
+  int n_pos, T, H, H_kv, d, rot, inverse, num_slots;
+  int* status;
+};
+cudaError_t launch_rope_rows(const RopeParams& p, int bf16, int layout, cudaStream_t stream);
+cudaError_t launch_rope_table_scaled(int seq_len, int rot, double base, int scaling, double factor, int orig_len,
+                                     double beta_fast, double beta_slow, float* table, cudaStream_t stream);
+
+// The page bookkeeping of one step (paged_step.cu): at most this many requests
+// (their prefix sums stay in one CTA's shared memory).
+constexpr int kPagedStepMaxRequests = 8192;
+cudaError_t launch_paged_step(const int* ctx_lens, const int* new_lens, int S, int* block_table, int max_pages,
+                              int* free_pages, int ring_size, const int* pool, int* pool_out, int page_size, int T,
+                              int* cu_q, int* kv_lens, int* positions, int* slots, int* info, cudaStream_t stream);
+
+// Attention of new tokens over a paged cache (extend.cu).
+struct ExtendShape {
+  int S, T, H, H_kv, d, max_new;
+};
+struct ExtendArgs {
+  ExtendShape n;
+  const void *q, *k_cache, *v_cache;
+  const int* block_table;
+  int max_pages, num_pages, page_size;
+  const void* plan;
+  const float* lambda;
+  float lambda_init;
+  const float* rms_w;
+  float eps;
+  int mode;
+  void* o;
+  void* workspace;
+};
+size_t extend_plan_bytes(const ExtendShape& n);
+size_t extend_workspace_bytes(const ExtendShape& n);
+cudaError_t launch_extend_plan(const int* cu_q, const int* kv_lens, const ExtendShape& n, int causal, void* plan,
+                               DevCtl ctl, cudaStream_t stream);
+cudaError_t launch_extend(const ExtendArgs& a, DevCtl ctl, cudaStream_t stream);
+
 }  // namespace diffattn

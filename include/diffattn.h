@@ -64,8 +64,9 @@ typedef enum {
   DIFFATTN_ERR_CUDA = 3,         /* a CUDA runtime/driver call failed         */
   DIFFATTN_ERR_TIMEOUT = 4,      /* a kernel's bounded wait ran out           */
   DIFFATTN_ERR_WORKSPACE = 5,    /* workspace missing or too small            */
-  DIFFATTN_ERR_BOUNDS = 6        /* debug build only: a kernel found an index
-                                    out of range and skipped the access       */
+  DIFFATTN_ERR_BOUNDS = 6        /* a kernel found an index out of range and
+                                    skipped the access (debug build; in the
+                                    paged calls and diffattn_rope always)     */
 } diffattn_status;
 
 typedef enum {
@@ -445,9 +446,167 @@ int diffattn_decode_noalloc(const void* q, const void* k_cache,
                             cudaStream_t stream);
 
 /*
+ * Serving from a paged cache.  A step of a server runs over S requests, each
+ * with some tokens cached and some new ones: one (generation), a few (drafted
+ * tokens to be checked), or a chunk of its prompt.  Their keys and values lie
+ * in pages of page_size tokens that belong to no request in particular:
+ *
+ *   k_cache : bf16 [num_pages, page_size, H_kv, 2, d]
+ *   v_cache : bf16 [num_pages, page_size, H_kv, 2d]
+ *   block_table : device int32 [S, max_pages]; entry j of row s is the page of
+ *             request s's tokens j * page_size .. (j + 1) * page_size - 1
+ *
+ * The new tokens' rows are packed: request s owns rows cu_q[s] .. cu_q[s+1]-1
+ * of T rows; rows from cu_q[S] on are padding and are left as they are.  One
+ * step is diffattn_paged_step and diffattn_extend_plan once, then per layer
+ * the projections, diffattn_kv_append and diffattn_extend.  All of it is
+ * stream-ordered and can be captured in one graph, with the lengths read on
+ * the device.
+ *
+ * diffattn_paged_step -- block tables and slot maps from the requests'
+ * lengths.
+ *   ctx_lens   : device int32[S], tokens cached before the step, >= 0
+ *   new_lens   : device int32[S], new tokens, >= 0; -1: the request is finished
+ *                and its pages are returned
+ *   block_table: entries ceil(ctx/page_size) .. ceil((ctx+new)/page_size) - 1
+ *                of each row are written, the others left
+ *   free_pages : device int32[ring_size], a ring of free pages: pool[1] of
+ *                them from index pool[0] on.  Pages are taken at its head in
+ *                the requests' order; returned pages (row order) are written
+ *                behind its tail and can be taken from the next step on.
+ *                ring_size must be at least the number of pages there are.
+ *   pool, pool_out : device int32[2], (head, count) before and after; they may
+ *                be the same buffer (then the step is not to be repeated)
+ *   T          : rows of positions and slots
+ *   cu_q       : device int32[S + 1], kv_lens : device int32[S] (ctx + new, 0
+ *                for a finished request), written
+ *   positions, slots : device int32[T], written: position in the request and
+ *                page * page_size + offset of every new token; -1 for padding
+ *   info       : device int32[4], written: new tokens, pages taken, pages
+ *                returned, and what is wrong, 0 or a sum of 1 (too few free
+ *                pages), 2 (a row needs more than max_pages pages), 4 (more
+ *                than T tokens), 8 (a length out of range) and 16 (pool does
+ *                not fit the ring).  Where it is not 0 nothing is taken or
+ *                returned: cu_q and kv_lens are 0, positions and slots -1,
+ *                pool_out is pool, and the other three values say what the
+ *                step would have needed (at most 2^31 - 1).
+ * S at most 8192 (DIFFATTN_ERR_UNSUPPORTED beyond); pointers 4-byte aligned.
+ */
+int diffattn_paged_step(const int* ctx_lens, const int* new_lens, int S, int* block_table, int max_pages,
+                        int* free_pages, int ring_size, const int* pool, int* pool_out, int page_size, int T,
+                        int* cu_q, int* kv_lens, int* positions, int* slots, int* info, cudaStream_t stream);
+
+/* Which channels form a rotated pair, for rot rotated channels. */
+typedef enum {
+  DIFFATTN_ROPE_INTERLEAVED = 0, /* (2j, 2j + 1): the layout of diffattn_qkv_proj */
+  DIFFATTN_ROPE_HALF = 1         /* (j, j + rot / 2)                              */
+} diffattn_rope_layout;
+
+/* How a table's frequencies theta_j = base^(-2j/rot) are scaled by `factor` s
+ * for contexts longer than the trained one. */
+typedef enum {
+  DIFFATTN_ROPE_PLAIN = 0,
+  DIFFATTN_ROPE_LINEAR = 1, /* theta_j / s (positions interpolated)                     */
+  DIFFATTN_ROPE_NTK = 2,    /* base * s^(rot / (rot - 2)) in place of base              */
+  DIFFATTN_ROPE_YARN = 3    /* theta_j (g_j + (1 - g_j) / s), with g_j rising linearly
+                               from 0 to 1 as the turns orig_len * theta_j / 2 pi go
+                               from beta_slow to beta_fast; cos and sin times
+                               0.1 ln s + 1                                             */
+} diffattn_rope_scaling;
+
+/*
+ * diffattn_rope_table_scaled -- table[n][j] = m (cos, sin) of n * theta'_j for
+ * the scaled frequencies above (double precision, rounded to float32).
+ *   table : device float32 [seq_len][rot / 2][2], written; rot even
+ *   factor >= 1 (unused for DIFFATTN_ROPE_PLAIN); orig_len >= 1 and
+ *   beta_fast > beta_slow >= 0 for DIFFATTN_ROPE_YARN (else unused)
+ * With DIFFATTN_ROPE_PLAIN and rot = d it is diffattn_rope_table's, and any
+ * table with rot = d can be given to diffattn_qkv_proj.
+ *
+ * diffattn_rope -- queries and keys rotated at given positions (after a
+ * projection without a table; packed or padded batches; part of the head).
+ *   q, q_out : [T, H, 2, d], k, k_out : [T, H_kv, 2, d], dtype F32 or BF16; the
+ *              outputs may be the inputs (and no other overlap); H_kv = 0: no k
+ *   positions: device int32[T]; a row with a negative position is padding and
+ *              its output is left as it is
+ *   table    : device float32 [n_pos][rot / 2][2], as the table calls write it
+ *   rot      : even, 2 <= rot <= d; channels from rot on are copied
+ *   inverse  : nonzero -> the transposed map (sin negated).  It takes the
+ *              gradient with respect to the outputs to that with respect to
+ *              the inputs; with m = 1 it is also the inverse.
+ * Float32 arithmetic, one rounding.  A position >= n_pos records
+ * DIFFATTN_ERR_BOUNDS in the device status word and leaves its row.
+ * d a multiple of 8 up to 256 (DIFFATTN_ERR_UNSUPPORTED otherwise).
+ *
+ * diffattn_kv_append -- the cache write of a step: q rotated into q_out, k
+ * rotated and v copied into the pages, in one launch.
+ *   q, q_out : bf16 [T, H, 2, d] (q_out may be q); k : bf16 [T, H_kv, 2, d];
+ *              v : bf16 [T, H_kv, 2d]
+ *   positions, table, n_pos, rot, layout : as in diffattn_rope; table NULL: no
+ *              rotation (positions, n_pos, rot and layout are not read and
+ *              every row of q is copied)
+ *   slots    : device int32[T]; a row with a negative slot writes no key or
+ *              value; one >= num_pages * page_size records
+ *              DIFFATTN_ERR_BOUNDS and writes none.  No slot may occur twice.
+ * Errors of the three: DIFFATTN_ERR_INVALID_ARG, DIFFATTN_ERR_UNSUPPORTED,
+ * DIFFATTN_ERR_CUDA.
+ */
+int diffattn_rope_table_scaled(int seq_len, int rot, double base, int scaling, double factor, int orig_len,
+                               double beta_fast, double beta_slow, float* table, cudaStream_t stream);
+int diffattn_rope(const void* q, const void* k, const int* positions, const float* table, int n_pos, int T, int H,
+                  int H_kv, int d, int rot, int dtype, int layout, int inverse, void* q_out, void* k_out,
+                  cudaStream_t stream);
+int diffattn_kv_append(const void* q, const void* k, const void* v, const int* positions, const int* slots,
+                       const float* table, int n_pos, int T, int H, int H_kv, int d, int rot, int layout,
+                       int num_pages, int page_size, void* q_out, void* k_cache, void* v_cache, cudaStream_t stream);
+
+/*
+ * diffattn_extend -- differential attention of every request's new tokens over
+ * its pages (the new tokens' own keys and values included, as
+ * diffattn_kv_append left them), with the headwise RMSNorm and the
+ * (1 - lambda_init) scale of diffattn_fwd.  Query i of a request with n new
+ * tokens and L = kv_lens[s] cached ones sees keys 0 .. L - n + i (causal) or
+ * all L.  A query that sees no key gives zeros.
+ *   q, o        : bf16 [T, H, 2, d] and [T, H, 2d]; H a multiple of H_kv, query
+ *                 heads g * H / H_kv .. (g + 1) * H / H_kv - 1 share key head g
+ *                 (at most 128 each); d = 64 or 128
+ *   page_size   : 16, 32, 64, 128 or 256
+ *   lambda, lambda_init, rms_w, eps, mode : as in diffattn_fwd_mode
+ *   plan        : the step's schedule, from diffattn_extend_plan with the same
+ *                 S, T, H, H_kv, d and max_new.  It is read only, so the calls
+ *                 of all layers, on any streams, may share it.
+ *   workspace   : device, >= diffattn_extend_workspace_size bytes (NULL if that
+ *                 is 0), 16-byte aligned, needs no initialisation.  Calls that
+ *                 overlap on the GPU (and graphs that are replayed at the same
+ *                 time) must not share one.
+ * diffattn_extend_plan -- writes the schedule of a step (>=
+ *   diffattn_extend_plan_size bytes, 16-byte aligned) from cu_q and kv_lens
+ *   (device, as diffattn_paged_step writes them).  max_new is a host bound of
+ *   the new tokens of a request.
+ * A request whose entries do not fit (negative, decreasing or beyond T, more
+ * than max_new new tokens, a negative length) records DIFFATTN_ERR_BOUNDS and
+ * its rows are left as they are.  Pages are checked against num_pages: one out of
+ * range, or a key beyond max_pages * page_size, records DIFFATTN_ERR_BOUNDS
+ * and reads as zeros.  Cached keys and values behind kv_lens, whatever they
+ * hold, do not enter the result; a plan of other sizes gives wrong results but
+ * no access out of bounds.
+ * Errors: DIFFATTN_ERR_INVALID_ARG, DIFFATTN_ERR_UNSUPPORTED,
+ * DIFFATTN_ERR_WORKSPACE (plan or workspace), DIFFATTN_ERR_CUDA;
+ * DIFFATTN_ERR_TIMEOUT through diffattn_device_status.
+ */
+size_t diffattn_extend_plan_size(int S, int T, int H, int H_kv, int d, int max_new);
+int diffattn_extend_plan(const int* cu_q, const int* kv_lens, int S, int T, int H, int H_kv, int d, int max_new,
+                         int causal, void* plan, size_t plan_bytes, cudaStream_t stream);
+size_t diffattn_extend_workspace_size(int S, int T, int H, int H_kv, int d, int max_new);
+int diffattn_extend(const void* q, const void* k_cache, const void* v_cache, const int* block_table, int max_pages,
+                    int num_pages, int page_size, const void* plan, size_t plan_bytes, int S, int T, int H, int H_kv,
+                    int d, int max_new, const float* lambda, float lambda_init, const float* rms_w, float eps,
+                    int mode, void* o, void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
  * diffattn_device_status -- synchronises the current device, then returns
- * the device-side status word (DIFFATTN_OK, DIFFATTN_ERR_TIMEOUT, or in the
- * debug build DIFFATTN_ERR_BOUNDS) in *status_out and clears it.  Returns DIFFATTN_ERR_CUDA if the device could
+ * the device-side status word (DIFFATTN_OK, DIFFATTN_ERR_TIMEOUT, or
+ * DIFFATTN_ERR_BOUNDS from the debug build and the paged calls) in *status_out and clears it.  Returns DIFFATTN_ERR_CUDA if the device could
  * not be queried.
  */
 int diffattn_device_status(int* status_out);
@@ -466,7 +625,8 @@ int diffattn_set_wait_limit_ns(long long limit_ns);
 const char* diffattn_status_string(int status);
 
 /* Library ABI version (major * 100 + minor); 101 adds the 4-bit pair
- * diffattn_quantize_qk4 / diffattn_fwd_qk4 to 100. */
+ * diffattn_quantize_qk4 / diffattn_fwd_qk4 to 100, 102 the paged serving calls
+ * (diffattn_paged_step, the rotary calls, diffattn_kv_append, diffattn_extend). */
 int diffattn_version(void);
 
 #ifdef __cplusplus

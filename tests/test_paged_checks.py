@@ -1,0 +1,109 @@
+"""Refusals of the paged serving calls, by the library and by the binding,
+before any CUDA call (no GPU needed)."""
+import ctypes
+
+import pytest
+import torch
+
+from differential_attention_04_b200 import _lib, api
+from differential_attention_04_b200.build import build
+
+INV, UNS, WS = api.ERR_INVALID_ARG, api.ERR_UNSUPPORTED, api.ERR_WORKSPACE
+nul, fake, odd = None, ctypes.c_void_p(4096), ctypes.c_void_p(4104)
+
+
+@pytest.fixture(scope="module")
+def L():
+    build()
+    return _lib.lib()
+
+
+def test_step_refusals(L):
+    f = lambda S=2, width=3, F=9, P=16, T=4, a=fake, pos=fake: L.diffattn_paged_step(
+        a, a, S, a, width, a, F, a, a, P, T, a, a, pos, pos, a, nul)
+    assert f(S=0) == INV and f(width=0) == INV and f(F=0) == INV and f(P=0) == INV and f(T=-1) == INV
+    assert f(a=nul) == INV and f(pos=nul) == INV and f(a=ctypes.c_void_p(4098)) == INV
+    assert f(S=8193) == UNS
+
+
+def test_rope_refusals(L):
+    t = lambda n=8, rot=64, base=1e4, kind=0, s=1.0, orig=4096, bf=32.0, bs=1.0, p=fake: \
+        L.diffattn_rope_table_scaled(n, rot, base, kind, s, orig, bf, bs, p, nul)
+    assert t(n=0) == INV and t(rot=7) == INV and t(rot=0) == INV and t(base=0.0) == INV and t(p=nul) == INV
+    assert t(kind=4) == INV and t(kind=-1) == INV and t(kind=1, s=0.5) == INV and t(kind=2, s=float("nan")) == INV
+    assert t(kind=2, rot=2, s=2.0) == INV and t(kind=3, s=2.0, orig=0) == INV and t(kind=3, s=2.0, bf=1.0) == INV
+    assert t(n=1 << 26) == INV
+    r = lambda q=fake, k=fake, pos=fake, tab=fake, n_pos=8, T=4, H=2, Hk=2, d=64, rot=64, dt=1, lay=0, qo=fake, \
+        ko=fake: L.diffattn_rope(q, k, pos, tab, n_pos, T, H, Hk, d, rot, dt, lay, 0, qo, ko, nul)
+    assert r(T=0) == api.OK and r(T=-1) == INV and r(H=0) == INV and r(Hk=-1) == INV
+    assert r(q=nul) == INV and r(k=nul) == INV and r(pos=nul) == INV and r(tab=nul) == INV and r(qo=nul) == INV
+    assert r(ko=nul) == INV and r(n_pos=0) == INV and r(rot=66) == INV and r(rot=7) == INV and r(rot=0) == INV
+    assert r(dt=2) == INV and r(lay=2) == INV and r(q=odd) == INV and r(ko=odd) == INV and r(d=60, rot=60) == UNS
+    assert r(d=264) == UNS and r(T=1 << 24) == INV
+    a = lambda q=fake, k=fake, pos=fake, sl=fake, tab=fake, T=4, H=2, Hk=2, d=64, rot=64, P=3, ps=16, kc=fake: \
+        L.diffattn_kv_append(q, k, k, pos, sl, tab, 8, T, H, Hk, d, rot, 0, P, ps, q, kc, kc, nul)
+    assert a(T=0) == api.OK and a(T=-1) == INV and a(Hk=0) == INV and a(q=nul) == INV and a(sl=nul) == INV
+    assert a(k=nul) == INV and a(kc=nul) == INV and a(kc=odd) == INV and a(P=0) == INV and a(ps=0) == INV
+    assert a(pos=nul) == INV and a(P=1 << 20, ps=1 << 12) == INV and a(d=60, rot=60) == UNS
+    assert a(tab=nul, pos=nul, d=60) == UNS and a(tab=nul, sl=nul) == INV
+
+
+def test_extend_refusals(L):
+    size = lambda S=2, T=8, H=4, Hk=2, d=64, mx=4: (L.diffattn_extend_plan_size(S, T, H, Hk, d, mx),
+                                                    L.diffattn_extend_workspace_size(S, T, H, Hk, d, mx))
+    assert size()[0] > 0
+    for bad in (dict(S=0), dict(T=-1), dict(H=0), dict(Hk=0), dict(Hk=3), dict(d=0), dict(d=96), dict(mx=-1),
+                dict(H=129, Hk=1), dict(S=1 << 16), dict(T=1 << 24)):
+        assert size(**bad) == (0, 0), bad
+    pl = lambda cu=fake, plan=fake, n=1 << 30, Hk=2, d=64: L.diffattn_extend_plan(cu, cu, 2, 8, 4, Hk, d, 4, 1, plan,
+                                                                                  n, nul)
+    assert pl(cu=nul) == INV and pl(plan=nul) == WS and pl(n=size()[0] - 1) == WS and pl(plan=odd) == WS
+    assert pl(Hk=3) == INV and pl(d=32) == UNS
+    ex = lambda q=fake, bt=fake, width=3, P=5, ps=16, plan=fake, pn=1 << 30, T=8, H=4, Hk=2, d=64, mx=4, eps=1e-5, \
+        mode=0, o=fake, ws=fake, wn=1 << 40: L.diffattn_extend(q, q, q, bt, width, P, ps, plan, pn, 2, T, H, Hk, d, mx,
+                                                               q, 0.5, q, eps, mode, o, ws, wn, nul)
+    assert ex(q=nul) == INV and ex(bt=nul) == INV and ex(o=nul) == INV and ex(width=0) == INV and ex(P=0) == INV
+    assert ex(ps=0) == INV and ex(ps=8) == UNS and ex(ps=48) == UNS and ex(ps=512) == UNS and ex(P=1 << 28) == INV
+    assert ex(eps=-1.0) == INV and ex(eps=float("nan")) == INV and ex(mode=3) == INV and ex(q=odd) == INV
+    assert ex(plan=nul) == WS and ex(pn=16) == WS and ex(Hk=3) == INV and ex(d=96) == UNS
+    assert ex(T=0) == api.OK and ex(mx=0) == api.OK
+    if size()[1]:
+        assert ex(ws=nul) == WS and ex(wn=8) == WS
+
+
+def _rejects(match, fn, *a, **k):
+    with pytest.raises(ValueError, match=match):
+        fn(*a, **k)
+
+
+def test_binding_refusals():
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)
+    dev = "must be CUDA tensors"
+    _rejects(dev, api.paged_step, i(2), i(2), i(2, 3), i(9), i(2), 16, 4)
+    _rejects("new_lens", api.paged_step, i(2), i(3), i(2, 3), i(9), i(2), 16, 4)
+    _rejects("ctx_lens", api.paged_step, i(2).long(), i(2), i(2, 3), i(9), i(2), 16, 4)
+    _rejects("pool", api.paged_step, i(2), i(2), i(2, 3), i(9), i(3), 16, 4)
+    _rejects("info", api.paged_step, i(2), i(2), i(2, 3), i(9), i(2), 16, 4, out=(i(3), i(2), i(4), i(4), i(3)))
+    bf = dict(dtype=torch.bfloat16)
+    q, k, v = torch.zeros(4, 4, 2, 64, **bf), torch.zeros(4, 2, 2, 64, **bf), torch.zeros(4, 2, 128, **bf)
+    tab, kc, vc = torch.zeros(9, 16, 2), torch.zeros(3, 16, 2, 2, 64, **bf), torch.zeros(3, 16, 2, 128, **bf)
+    _rejects(dev, api.rope, q, k, i(4), tab)
+    _rejects(dev, api.rope, q, None, i(4), tab, inverse=True)
+    _rejects("positions", api.rope, q, k, i(3), tab)
+    _rejects("k must be", api.rope, q, k.float(), i(4), tab)
+    _rejects("table", api.rope, q, k, i(4), torch.zeros(9, 33, 2))
+    _rejects("dtype", api.rope, q.half(), None, i(4), tab)
+    _rejects(dev, api.kv_append, q, k, v, i(4), i(4), tab, kc, vc)
+    _rejects(dev, api.kv_append, q, k, v, None, i(4), None, kc, vc)
+    _rejects("slots", api.kv_append, q, k, v, i(4), i(5), tab, kc, vc)
+    _rejects("positions", api.kv_append, q, k, v, None, i(4), tab, kc, vc)
+    _rejects("v_cache", api.kv_append, q, k, v, i(4), i(4), tab, kc, vc[:2])
+    _rejects("k must be", api.kv_append, q, k[:, :1], v, i(4), i(4), tab, kc, vc)
+    _rejects(dev, api.extend_plan, i(3), i(2), 4, 4, 2, 64, 4)
+    _rejects("cu_q", api.extend_plan, i(2), i(2), 4, 4, 2, 64, 4)
+    plan = api.ExtendPlan(torch.zeros(1 << 16, dtype=torch.uint8), 2, 4, 4, 2, 64, 4)
+    lam, w = torch.zeros(1), torch.ones(128)
+    _rejects(dev, api.diffattn_extend, q, kc, vc, i(2, 3), plan, lam, 0.5, w)
+    _rejects("other sizes", api.diffattn_extend, q[:3], kc, vc, i(2, 3), plan, lam, 0.5, w)
+    _rejects("block_table", api.diffattn_extend, q, kc, vc, i(3, 3), plan, lam, 0.5, w)
+    _rejects("rms_w", api.diffattn_extend, q, kc, vc, i(2, 3), plan, lam, 0.5, w[:64])
