@@ -1,6 +1,5 @@
-// Differential attention of new tokens over a paged cache, d in {64, 128},
-// bf16 in and out, float32 arithmetic: the schedule of a step and the plain
-// kernel.
+// Differential attention of new tokens over a paged cache: the schedule of a
+// step, the joining of split rows, and the launches.
 //
 // Query i of a request with n new tokens and L cached ones (the new ones
 // included) sees keys 0 .. L - n + i (causal) or all L; a row that sees no key
@@ -10,137 +9,359 @@
 #include <math.h>
 
 #include "common.cuh"
-#include "internal.h"
+#include "extend.cuh"
 
 namespace diffattn {
 
 namespace {
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kWarps = 4;
 
-__device__ __forceinline__ void note_bounds(int* status) { atomicCAS(status, 0, 6); }
+constexpr int kPlanThreads = 1024;
 
-// Per token: (request, last visible key); request -1 for rows behind the last one.
-__global__ void extend_plan_kernel(const int* __restrict__ cu, const int* __restrict__ kvl, ExtendShape n, int causal,
-                                   int2* tok, int* status) {
-  const int t = blockIdx.x * blockDim.x + threadIdx.x;
-  if (t >= n.T) return;
-  int2 e = make_int2(-1, -1);
-  if (t < cu[n.S]) {
-    int lo = 0, hi = n.S - 1;
-    while (lo < hi) {
-      const int m = (lo + hi + 1) >> 1;
-      if (cu[m] <= t) lo = m;
-      else hi = m - 1;
-    }
-    const int nq = cu[lo + 1] - cu[lo], L = kvl[lo];
-    if (nq > n.max_new || L < 0) note_bounds(status);
-    else e = make_int2(lo, causal ? L - nq + (t - cu[lo]) : L - 1);
-  }
-  tok[t] = e;
+struct PlanSums {
+  long long units;
+  int reqs, tiles, top;  // top: the largest offset so far (a maximum, not a sum)
+};
+
+__device__ __forceinline__ PlanSums plan_add(const PlanSums& a, const PlanSums& b) {
+  return PlanSums{a.units + b.units, a.reqs + b.reqs, a.tiles + b.tiles, max(a.top, b.top)};
 }
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) extend_plain_kernel(const ExtendArgs a, int* status) {
-  constexpr int E = 2 * D / 32;  // elements of a row per lane
-  const int t = blockIdx.x, h = blockIdx.y, hk = h / (a.n.H / a.n.H_kv);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, map = lane >> 4;
-  const int2 e = static_cast<const int2*>(a.plan)[t];
-  if (e.x < 0) return;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (static_cast<size_t>(t) * a.n.H + h) * 2 * D;
-  float qf[E], o[2][E], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+// Exclusive scan over the block (identity: zeros and the smallest int); `total` gets the block's.
+__device__ __forceinline__ PlanSums plan_scan(PlanSums v, PlanSums* sm, PlanSums& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  PlanSums x = v;
+  auto up = [](const PlanSums& a, int off) {
+    return PlanSums{__shfl_up_sync(0xffffffffu, a.units, off), __shfl_up_sync(0xffffffffu, a.reqs, off),
+                    __shfl_up_sync(0xffffffffu, a.tiles, off), __shfl_up_sync(0xffffffffu, a.top, off)};
+  };
+  const PlanSums none{0, 0, 0, static_cast<int>(0x80000000)};
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    qf[i] = __bfloat162float(q[E * lane + i]) * (kLog2e * rsqrtf(static_cast<float>(D)));
-    o[0][i] = o[1][i] = 0.f;
+  for (int off = 1; off < 32; off <<= 1) {
+    const PlanSums o = up(x, off);
+    if (lane >= off) x = plan_add(o, x);
   }
-  const __nv_bfloat16* kc = static_cast<const __nv_bfloat16*>(a.k_cache);
-  const __nv_bfloat16* vc = static_cast<const __nv_bfloat16*>(a.v_cache);
-  for (int key = warp; key <= e.y; key += kWarps) {
-    const int j = key / a.page_size;
-    const int page = j < a.max_pages ? a.block_table[static_cast<size_t>(e.x) * a.max_pages + j] : -1;
-    const bool ok = page >= 0 && page < a.num_pages;
-    if (!ok) note_bounds(status);
-    const size_t row = ((static_cast<size_t>(ok ? page : 0) * a.page_size + key % a.page_size) * a.n.H_kv + hk) * 2 * D;
-    float s = 0.f, v[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      s = fmaf(qf[i], ok ? __bfloat162float(kc[row + E * lane + i]) : 0.f, s);
-      v[i] = ok ? __bfloat162float(vc[row + E * lane + i]) : 0.f;
-    }
-#pragma unroll
-    for (int off = 8; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    const float other = __shfl_xor_sync(0xffffffffu, s, 16);
-    const float sc[2] = {map ? other : s, map ? s : other};
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const float mn = fmaxf(m[w], sc[w]), al = fast_exp2(m[w] - mn), p = fast_exp2(sc[w] - mn);
-      m[w] = mn;
-      l[w] = l[w] * al + p;
-#pragma unroll
-      for (int i = 0; i < E; ++i) o[w][i] = fmaf(o[w][i], al, p * v[i]);
-    }
+  if (lane == 31) sm[warp] = x;
+  __syncthreads();
+  PlanSums before = none;
+  total = none;
+#pragma unroll 4
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w == warp) before = total;
+    total = plan_add(total, sm[w]);
   }
-  __shared__ float sm_m[kWarps][2], sm_l[kWarps][2], sm_o[kWarps][2][2 * D], red[kWarps];
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    if (lane == 0) {
-      sm_m[warp][w] = m[w];
-      sm_l[warp][w] = l[w];
+  __syncthreads();  // sm is reused
+  const PlanSums prev = up(x, 1);
+  return lane == 0 ? before : plan_add(before, prev);
+}
+
+__device__ __forceinline__ int units_of(long long keys) {
+  return keys <= 0 ? 1 : static_cast<int>((keys + kUnit - 1) / kUnit);
+}
+
+// The last i < n with pre[i] <= u (pre[0] = 0, non-decreasing).
+template <class F>
+__device__ __forceinline__ int last_at_most(int lo, int hi, long long u, F pre) {
+  while (lo < hi) {
+    const int m = static_cast<int>((static_cast<long long>(lo) + hi + 1) >> 1);
+    if (pre(m) <= u) lo = m;
+    else hi = m - 1;
+  }
+  return lo;
+}
+
+// One CTA: it reads each length once, and the two lists are short.  Latency-
+// bound (block scans and, per worker, two binary searches in L2); a step pays
+// it once for all layers.
+__global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __restrict__ cu,
+                                                                   const int* __restrict__ kvl, ExtendShape n,
+                                                                   int causal, int wide_workers, char* plan,
+                                                                   int* status) {
+  __shared__ PlanSums sm[kPlanThreads / 32];
+  const PlanLayout lay = plan_layout(n);
+  PlanHeader* head = reinterpret_cast<PlanHeader*>(plan);
+  NarrowReq* narrow = reinterpret_cast<NarrowReq*>(plan + lay.narrow);
+  WideTile* wide = reinterpret_cast<WideTile*>(plan + lay.wide);
+  long long* npre = reinterpret_cast<long long*>(plan + lay.narrow_pre);
+  long long* wpre = reinterpret_cast<long long*>(plan + lay.wide_pre);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int G = n.H / n.H_kv, tpt = kWideRows / G;
+
+  // the requests, into the two lists
+  PlanSums carry{0, 0, 0, 0};
+  for (int base = 0; base < n.S; base += kPlanThreads) {
+    const int s = base + tid;
+    int q0 = 0, nq = 0, L = 0;
+    bool mine = s < n.S;
+    PlanSums v{0, 0, 0, static_cast<int>(0x80000000)};
+    if (mine) {
+      q0 = cu[s];
+      const long long end = cu[s + 1];
+      L = kvl[s];
+      // offsets must not fall below an earlier one: then no two requests share rows, and
+      // the row tiles fit their list
+      v.top = q0;
+      nq = q0 < 0 || end < q0 || end > n.T || L < 0 || L > kMaxKeys || end - q0 > n.max_new ? -1 : static_cast<int>(end - q0);
     }
-#pragma unroll
-    for (int i = 0; i < E; ++i) sm_o[warp][w][E * lane + i] = o[w][i];
+    // whether it fits is only known with the largest earlier offset, so that is scanned first
+    PlanSums total;
+    const PlanSums before = plan_scan(v, sm, total);
+    if (mine && (nq < 0 || q0 < max(carry.top, before.top))) {
+      atomicCAS(status, 0, 6);
+      nq = -1;
+    }
+    carry.top = max(carry.top, total.top);
+    const bool is_wide = static_cast<long long>(nq) * G > kNarrowRows;
+    v = PlanSums{0, 0, 0, static_cast<int>(0x80000000)};
+    if (nq > 0 && !is_wide) {
+      v.reqs = 1;
+      v.units = static_cast<long long>(units_of(L)) * n.H_kv;
+    }
+    if (is_wide) v.tiles = (nq + tpt - 1) / tpt;
+    const PlanSums at = plan_scan(v, sm, total);
+    if (v.reqs) {
+      const int i = carry.reqs + at.reqs;
+      narrow[i] = NarrowReq{q0, nq, L, s};
+      npre[i] = carry.units + at.units;
+    }
+    // a warp writes the row tiles of one request at a time
+    for (unsigned todo = __ballot_sync(0xffffffffu, v.tiles > 0); todo; todo &= todo - 1) {
+      const int from = __ffs(todo) - 1;
+      const int first = __shfl_sync(0xffffffffu, carry.tiles + at.tiles, from);
+      const int cnt = __shfl_sync(0xffffffffu, v.tiles, from), fq = __shfl_sync(0xffffffffu, q0, from);
+      const int fn = __shfl_sync(0xffffffffu, nq, from), fL = __shfl_sync(0xffffffffu, L, from);
+      const int fs = __shfl_sync(0xffffffffu, s, from);
+      for (int i = lane; i < cnt && first + i < lay.max_tiles; i += 32) {
+        WideTile w;
+        w.tok0 = fq + i * tpt;
+        w.ntok = min(tpt, fn - i * tpt);
+        w.lim0 = causal ? fL - fn + i * tpt : fL - 1;
+        w.units = units_of(causal ? static_cast<long long>(w.lim0) + w.ntok : fL);
+        w.L = fL;
+        w.s = fs;
+        w.first = first;
+        w.count = cnt;
+        wide[first + i] = w;
+      }
+    }
+    carry.reqs += total.reqs;
+    carry.tiles += total.tiles;
+    carry.units += total.units;
+  }
+  const int nreqs = carry.reqs, ntiles = min(carry.tiles, lay.max_tiles);
+  const long long nunits = carry.units;
+  __syncthreads();  // the tiles are read by other threads
+  long long wunits = 0;  // per key head
+  for (int base = 0; base < ntiles; base += kPlanThreads) {
+    const int x = base + tid;
+    const PlanSums v{x < ntiles ? wide[x].units : 0, 0, 0, 0};
+    PlanSums total;
+    const PlanSums at = plan_scan(v, sm, total);
+    if (x < ntiles) wpre[x] = wunits + at.units;
+    wunits += total.units;
+  }
+  if (tid == 0) {
+    npre[nreqs] = nunits;
+    wpre[ntiles] = wunits;
   }
   __syncthreads();
-  const float c2 = map2_coefficient(a.mode, *a.lambda);
-  float y[2 * D / (kWarps * 32)], ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < 2 * D / (kWarps * 32); ++i) {
-    const int c = threadIdx.x + i * kWarps * 32;
-    float ov = 0.f;
-    for (int w = 0; w < 2; ++w) {
-      float M = -INFINITY, L = 0.f, x = 0.f;
-      for (int g = 0; g < kWarps; ++g) M = fmaxf(M, sm_m[g][w]);
-      for (int g = 0; g < kWarps; ++g) {
-        const float f = M == -INFINITY ? 0.f : fast_exp2(sm_m[g][w] - M);
-        L = fmaf(f, sm_l[g][w], L);
-        x = fmaf(f, sm_o[g][w][c], x);
-      }
-      ov += L > 0.f ? (w ? c2 : 1.f) * x / L : 0.f;
-    }
-    y[i] = ov;
-    ss = fmaf(ov, ov, ss);
+  const long long U[2] = {nunits, wunits * n.H_kv};
+  const int W[2] = {static_cast<int>(min(U[0], static_cast<long long>(kNarrowWorkers))),
+                    static_cast<int>(min(U[1], static_cast<long long>(wide_workers)))};
+  if (tid == 0) {
+    *head = PlanHeader{{U[0], U[1]}, {W[0], W[1]}, causal, ntiles, n, kPlanMagic, 0};
   }
+  // the workers: where each begins, and the item that it leaves unfinished
+  for (int i = tid; i < kNarrowWorkers + kWideWorkers; i += kPlanThreads) {
+    const int c = i >= kNarrowWorkers, w = c ? i - kNarrowWorkers : i;
+    WorkStart st{0, 0, 0, 0};
+    WorkTail tl{0, 0, 0, 0};
+    if (w < W[c]) {
+      // the item of unit u: (list index, key head), its first unit and the one behind its last
+      auto item = [&](long long u, int* hk, long long* b, long long* e) -> int {
+        if (c == 0) {
+          const int r = last_at_most(0, nreqs - 1, u, [&](int k) { return npre[k]; });
+          const long long per = (npre[r + 1] - npre[r]) / n.H_kv;
+          *hk = static_cast<int>((u - npre[r]) / per);
+          *b = npre[r] + *hk * per;
+          *e = *b + per;
+          return r;
+        }
+        const int any = last_at_most(0, ntiles - 1, u, [&](int k) { return wpre[wide[k].first] * n.H_kv; });
+        const int first = wide[any].first, cnt = wide[any].count;
+        const long long off = wpre[first], per = wpre[first + cnt] - off;
+        *hk = static_cast<int>((u - off * n.H_kv) / per);
+        const long long base = off * n.H_kv + *hk * per;
+        const int x = last_at_most(first, first + cnt - 1, u - base, [&](int k) { return wpre[k] - off; });
+        *b = base + wpre[x] - off;
+        *e = base + wpre[x + 1] - off;
+        return x;
+      };
+      auto start_of = [&](long long v) { return v * U[c] / W[c]; };
+      const long long u0 = start_of(w), u1 = start_of(w + 1);
+      int hk;
+      long long b, e;
+      const int at = item(u0, &hk, &b, &e);
+      st = WorkStart{at, hk, static_cast<int>(u0 - b), static_cast<int>(u1 - u0)};
+      const int last = item(u1 - 1, &hk, &b, &e);
+      if (b >= u0 && e > u1) {
+        int parts = 1;
+        while (w + parts < W[c] && start_of(w + parts) < e) ++parts;
+        tl = WorkTail{last, hk, parts, 0};
+      }
+    }
+    reinterpret_cast<WorkStart*>(plan + lay.starts[c])[w] = st;
+    reinterpret_cast<WorkTail*>(plan + lay.tails[c])[w] = tl;
+  }
+}
+
+// Joins the rows that were split: block (worker, row) adds the parts of the
+// item that the worker began, each taken to the common maximum, in the order
+// of the keys within eight groups of parts and then group by group; then the
+// epilogue of a whole row.  Reads 16 d bytes a part and row.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinGroups = kJoinThreads / 32;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) extend_join_kernel(const ExtendArgs a, const float* nrecs,
+                                                                   const float* wrecs, int* status) {
+  constexpr int DV = 2 * D;
+  if (!plan_fits(a.plan, a.n, status)) return;
+  const bool is_wide = blockIdx.x >= kNarrowWorkers * kNarrowRows;
+  const int bi = is_wide ? blockIdx.x - kNarrowWorkers * kNarrowRows : blockIdx.x;
+  const int rows = is_wide ? kWideRows : kNarrowRows;
+  const int w = bi / rows, r = bi % rows;
+  const PlanView pv = plan_view(a.plan, a.n, is_wide);
+  const WorkTail tl = pv.tails[w];
+  if (tl.parts == 0) return;
+  const int G = a.n.H / a.n.H_kv;
+  const int tok0 = is_wide ? pv.wide[tl.at].tok0 : pv.narrow[tl.at].q0;
+  const int ntok = is_wide ? pv.wide[tl.at].ntok : pv.narrow[tl.at].n;
+  if (r >= ntok * G) return;
+  const float* recs = is_wide ? wrecs : nrecs;
+  const size_t rec = record_floats(rows, D);
+  const int tid = threadIdx.x, lane = tid & 31, grp = tid >> 5;
+  // part p of worker w's item: its own last record, then the first records of the workers behind it
+  auto part = [&](int p) { return recs + (p == 0 ? 2 * w + 1 : 2 * (w + p)) * rec; };
+
+  __shared__ float2 f[kNarrowWorkers];  // factors of a part's two maps
+  __shared__ float red[4][kJoinGroups];
+  __shared__ float acc[kJoinGroups][2 * DV];
+  static_assert(kNarrowWorkers <= kJoinThreads, "one thread per part");
+  float4 ml = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+  if (tid < tl.parts) ml = *reinterpret_cast<const float4*>(part(tid) + 4 * r);
+  float M1 = ml.x, M2 = ml.z;
+#pragma unroll
+  for (int off = 16; off; off >>= 1) {
+    M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, off));
+    M2 = fmaxf(M2, __shfl_xor_sync(0xffffffffu, M2, off));
+  }
+  if (lane == 0) {
+    red[0][grp] = M1;
+    red[1][grp] = M2;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int g = 0; g < kJoinGroups; ++g) {
+    M1 = fmaxf(M1, red[0][g]);
+    M2 = fmaxf(M2, red[1][g]);
+  }
+  const float f1 = M1 == -INFINITY ? 0.f : fast_exp2(ml.x - M1), f2 = M2 == -INFINITY ? 0.f : fast_exp2(ml.z - M2);
+  if (tid < tl.parts) f[tid] = make_float2(f1, f2);
+  float l1 = f1 * ml.y, l2 = f2 * ml.w;
+#pragma unroll
+  for (int off = 16; off; off >>= 1) {
+    l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+    l2 += __shfl_xor_sync(0xffffffffu, l2, off);
+  }
+  if (lane == 0) {
+    red[2][grp] = l1;
+    red[3][grp] = l2;
+  }
+  __syncthreads();
+  constexpr int NV = 2 * DV / 128;  // float4 per lane: both maps' channels
+  float4 x[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int p = grp; p < tl.parts; p += kJoinGroups) {
+    const float2 fp = f[p];
+    const float4* o = reinterpret_cast<const float4*>(part(p) + 4 * rows + static_cast<size_t>(r) * 2 * DV);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float4 v = __ldg(o + 32 * i + lane);
+      const float fi = i < NV / 2 ? fp.x : fp.y;
+      x[i].x = fmaf(fi, v.x, x[i].x);
+      x[i].y = fmaf(fi, v.y, x[i].y);
+      x[i].z = fmaf(fi, v.z, x[i].z);
+      x[i].w = fmaf(fi, v.w, x[i].w);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) *reinterpret_cast<float4*>(&acc[grp][4 * (32 * i + lane)]) = x[i];
+  __syncthreads();
+  float y = 0.f;
+  if (tid < DV) {
+    float o1 = 0.f, o2 = 0.f;
+    l1 = l2 = 0.f;
+#pragma unroll
+    for (int g = 0; g < kJoinGroups; ++g) {
+      o1 += acc[g][tid];
+      o2 += acc[g][DV + tid];
+      l1 += red[2][g];
+      l2 += red[3][g];
+    }
+    y = (l1 > 0.f ? o1 / l1 : 0.f) + map2_coefficient(a.mode, *a.lambda) * (l2 > 0.f ? o2 / l2 : 0.f);
+  }
+  float ss = y * y;
 #pragma unroll
   for (int off = 16; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-  if (lane == 0) red[warp] = ss;
   __syncthreads();
-  ss = red[0] + red[1] + red[2] + red[3];
-  const float gsc = (1.f - a.lambda_init) * rsqrtf(ss / (2 * D) + a.eps);
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + (static_cast<size_t>(t) * a.n.H + h) * 2 * D;
+  if (lane == 0) red[0][grp] = ss;
+  __syncthreads();
+  ss = 0.f;
 #pragma unroll
-  for (int i = 0; i < 2 * D / (kWarps * 32); ++i) {
-    const int c = threadIdx.x + i * kWarps * 32;
-    out[c] = __float2bfloat16_rn(y[i] * gsc * a.rms_w[c]);
+  for (int g = 0; g < kJoinGroups; ++g) ss += red[0][g];
+  if (tid < DV) {
+    const float gsc = (1.f - a.lambda_init) * rsqrtf(ss / DV + a.eps);
+    const size_t row = static_cast<size_t>(tok0 + r / G) * a.n.H + static_cast<size_t>(tl.hk) * G + r % G;
+    static_cast<__nv_bfloat16*>(a.o)[row * DV + tid] = __float2bfloat16_rn(y * gsc * a.rms_w[tid]);
   }
+}
+
+size_t narrow_record_bytes(const ExtendShape& n) {
+  return 2 * kNarrowWorkers * record_floats(kNarrowRows, n.d) * sizeof(float);
 }
 }  // namespace
 
-size_t extend_plan_bytes(const ExtendShape& n) { return static_cast<size_t>(n.T > 0 ? n.T : 1) * sizeof(int2) + 16; }
-size_t extend_workspace_bytes(const ExtendShape&) { return 0; }
+size_t extend_plan_bytes(const ExtendShape& n) { return plan_layout(n).bytes; }
+
+size_t extend_workspace_bytes(const ExtendShape& n) {
+  size_t b = narrow_record_bytes(n);
+  if (wide_possible(n)) b += 2 * kWideWorkers * record_floats(kWideRows, n.d) * sizeof(float);
+  return b;
+}
 
 cudaError_t launch_extend_plan(const int* cu_q, const int* kv_lens, const ExtendShape& n, int causal, void* plan,
                                DevCtl ctl, cudaStream_t stream) {
-  if (n.T == 0) return cudaSuccess;
-  extend_plan_kernel<<<(n.T + 255) / 256, 256, 0, stream>>>(cu_q, kv_lens, n, causal, static_cast<int2*>(plan),
-                                                            ctl.status);
+  extend_plan_kernel<<<1, kPlanThreads, 0, stream>>>(cu_q, kv_lens, n, causal ? 1 : 0, kWideWorkers,
+                                                     static_cast<char*>(plan), ctl.status);
   return cudaGetLastError();
 }
 
 cudaError_t launch_extend(const ExtendArgs& a, DevCtl ctl, cudaStream_t stream) {
-  const dim3 grid(a.n.T, a.n.H);
-  if (a.n.d == 128) extend_plain_kernel<128><<<grid, kWarps * 32, 0, stream>>>(a, ctl.status);
-  else extend_plain_kernel<64><<<grid, kWarps * 32, 0, stream>>>(a, ctl.status);
+  float* nrecs = static_cast<float*>(a.workspace);
+  float* wrecs = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + narrow_record_bytes(a.n));
+  const bool wide = wide_possible(a.n);
+  cudaError_t e = launch_extend_narrow(a, nrecs, ctl, stream);
+  if (e != cudaSuccess) return e;
+  if (wide && (e = launch_extend_wide(a, wrecs, ctl, stream)) != cudaSuccess) return e;
+  // no item can be split where every request's keys fit one unit
+  if (!wide && static_cast<long long>(a.max_pages) * a.page_size <= kUnit) return cudaSuccess;
+  const unsigned grid = kNarrowWorkers * kNarrowRows;
+  if (a.n.d == 128)
+    extend_join_kernel<128><<<grid, kJoinThreads, 0, stream>>>(a, nrecs, wrecs, ctl.status);
+  else
+    extend_join_kernel<64><<<grid, kJoinThreads, 0, stream>>>(a, nrecs, wrecs, ctl.status);
   return cudaGetLastError();
 }
 

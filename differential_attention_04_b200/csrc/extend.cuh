@@ -1,0 +1,125 @@
+// Schedule of a serving step's attention, shared by the plan kernel, the two
+// attention kernels and the kernel that joins split rows.
+//
+// A request's query rows are its new tokens times the G = H / H_kv query heads
+// that share a key head.  Requests of at most kNarrowRows rows are "narrow"
+// (extend_narrow.cu: memory-bound), the others "wide" (extend_wide.cu: tiles of
+// up to 128 rows on the tensor cores).  An item is one (request, key head) of
+// the narrow class or one (row tile, key head) of the wide class; its work is
+// its number of units, blocks of kUnit keys that its last row can see (at
+// least one, so that rows without keys are written too).  The items of a class
+// lie end to end on a line of units, request by request, then key head by key
+// head, then row tile by row tile; worker w of W takes units
+// floor(w U / W) .. floor((w + 1) U / W) - 1.  So all workers get the same
+// work (to one unit) whatever the lengths, and only a worker's first and last
+// items can be split: their unnormalised sums go to the workspace records
+// 2 w (the item began before the worker's range) and 2 w + 1 (it began inside
+// it and goes on behind it), which the joining kernel adds up in order.
+#pragma once
+
+#include "internal.h"
+
+namespace diffattn {
+
+constexpr int kUnit = 128;
+constexpr int kNarrowRows = 8;
+constexpr int kWideRows = 128;
+constexpr int kNarrowWorkers = 148;  // one CTA per SM
+constexpr int kWideWorkers = 74;     // one CTA pair per two SMs
+
+struct PlanHeader {
+  long long units[2];  // of the narrow and the wide class
+  int workers[2];      // workers with units
+  int causal;
+  int tiles;           // entries of the list of row tiles
+  ExtendShape shape;   // the sizes that the plan was made for
+  int magic, pad;
+};
+constexpr int kPlanMagic = 0x64706c6e;
+constexpr int kMaxKeys = 0x7fffff00;  // keys of a request: a unit behind the last one still has a 32-bit index
+static_assert(sizeof(PlanHeader) == 64, "the sections behind the header are 16-byte aligned");
+
+struct NarrowReq {
+  int q0, n, L, s;  // first row, new tokens, cached tokens, request
+};
+struct WideTile {
+  int tok0, ntok;       // its tokens' rows
+  int lim0;             // last key its first token sees (causal: one more per token)
+  int units;            // units per key head
+  int L, s, first, count;  // cached tokens, request; the request's first row tile and their number
+};
+// Where a worker begins: item (at, hk), its unit, and how many units it takes.
+// Its tail: the item (at, hk) that it began and did not finish, and in how many parts (0: none).
+struct WorkStart {
+  int at, hk, unit, count;
+};
+struct WorkTail {
+  int at, hk, parts, pad;
+};
+
+struct PlanLayout {
+  size_t starts[2], tails[2], narrow, narrow_pre, wide, wide_pre, bytes;
+  int max_tiles;  // row tiles of the wide class there can be
+};
+
+__host__ __device__ inline bool wide_possible(const ExtendShape& n) {
+  return static_cast<long long>(n.max_new) * (n.H / n.H_kv) > kNarrowRows;
+}
+
+__host__ __device__ inline PlanLayout plan_layout(const ExtendShape& n) {
+  PlanLayout l;
+  const int tpt = kWideRows / (n.H / n.H_kv);
+  l.max_tiles = wide_possible(n) ? n.T / tpt + n.S : 0;
+  size_t at = sizeof(PlanHeader);
+  const int workers[2] = {kNarrowWorkers, kWideWorkers};
+  for (int c = 0; c < 2; ++c) {
+    l.starts[c] = at;
+    at += workers[c] * sizeof(WorkStart);
+    l.tails[c] = at;
+    at += workers[c] * sizeof(WorkTail);
+  }
+  l.narrow = at;
+  at += static_cast<size_t>(n.S) * sizeof(NarrowReq);
+  l.wide = at;
+  at += static_cast<size_t>(l.max_tiles) * sizeof(WideTile);
+  l.narrow_pre = at;
+  at += (static_cast<size_t>(n.S) + 1) * sizeof(long long);
+  l.wide_pre = at;
+  at += (static_cast<size_t>(l.max_tiles) + 1) * sizeof(long long);
+  l.bytes = (at + 15) & ~static_cast<size_t>(15);
+  return l;
+}
+
+// A record: (m1, l1, m2, l2) of every row, then per row both maps' sums over 2d channels.
+__host__ __device__ inline size_t record_floats(int rows, int d) {
+  return static_cast<size_t>(rows) * (4 + 4 * d);
+}
+
+struct PlanView {
+  const PlanHeader* head;
+  const WorkStart* starts;
+  const WorkTail* tails;
+  const NarrowReq* narrow;
+  const WideTile* wide;
+};
+// Whether the buffer holds a plan of these sizes; the kernels do nothing otherwise.
+__device__ inline bool plan_fits(const void* plan, const ExtendShape& n, int* status) {
+  const PlanHeader* h = static_cast<const PlanHeader*>(plan);
+  const ExtendShape& p = h->shape;
+  const bool ok = h->magic == kPlanMagic && p.S == n.S && p.T == n.T && p.H == n.H && p.H_kv == n.H_kv &&
+                  p.d == n.d && p.max_new == n.max_new;
+  if (!ok) atomicCAS(status, 0, 6);
+  return ok;
+}
+__device__ inline PlanView plan_view(const void* plan, const ExtendShape& n, int cls) {
+  const PlanLayout l = plan_layout(n);
+  const char* p = static_cast<const char*>(plan);
+  return PlanView{reinterpret_cast<const PlanHeader*>(p), reinterpret_cast<const WorkStart*>(p + l.starts[cls]),
+                  reinterpret_cast<const WorkTail*>(p + l.tails[cls]),
+                  reinterpret_cast<const NarrowReq*>(p + l.narrow), reinterpret_cast<const WideTile*>(p + l.wide)};
+}
+
+cudaError_t launch_extend_narrow(const ExtendArgs& a, float* recs, DevCtl ctl, cudaStream_t stream);
+cudaError_t launch_extend_wide(const ExtendArgs& a, float* recs, DevCtl ctl, cudaStream_t stream);
+
+}  // namespace diffattn

@@ -585,11 +585,13 @@ int diffattn_kv_append(const void* q, const void* k, const void* v, const int* p
  *   the new tokens of a request.
  * A request whose entries do not fit (negative, decreasing or beyond T, more
  * than max_new new tokens, a negative length) records DIFFATTN_ERR_BOUNDS and
- * its rows are left as they are.  Pages are checked against num_pages: one out of
- * range, or a key beyond max_pages * page_size, records DIFFATTN_ERR_BOUNDS
- * and reads as zeros.  Cached keys and values behind kv_lens, whatever they
- * hold, do not enter the result; a plan of other sizes gives wrong results but
- * no access out of bounds.
+ * its rows are left as they are.  Pages are checked against num_pages: one out
+ * of range records DIFFATTN_ERR_BOUNDS and reads as zeros.  Keys from
+ * max_pages * page_size on record it too and do not enter.  Cached keys and
+ * values behind kv_lens, whatever they hold, do not enter the result; those
+ * before it must be finite (one that a query may not see enters with weight
+ * zero).  A plan of other sizes, or none, records DIFFATTN_ERR_BOUNDS and
+ * nothing is computed.
  * Errors: DIFFATTN_ERR_INVALID_ARG, DIFFATTN_ERR_UNSUPPORTED,
  * DIFFATTN_ERR_WORKSPACE (plan or workspace), DIFFATTN_ERR_CUDA;
  * DIFFATTN_ERR_TIMEOUT through diffattn_device_status.

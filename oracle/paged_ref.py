@@ -93,7 +93,7 @@ def rope(x, pos, theta, m=1.0, half=False, inverse=False):
 def extend(q, k_cache, v_cache, table, cu_q, kv_lens, lam, lambda_init, rms_w, eps, causal=True, c2=None,
            p_err=None, out_err=0.0):
     """[T, H, 2d]; rows of no request are nan.  c2: the coefficient of map 2 (default -lam).  Pages out of range
-    read as zeros.
+    read as zeros; keys that the table has no entry for are left out.
 
     With p_err, also a bound of the error of an implementation whose weights are off by at most p_err relative
     (and whose result is rounded by at most out_err relative): the sum o of c_i p_i v is off by at most
@@ -107,15 +107,15 @@ def extend(q, k_cache, v_cache, table, cu_q, kv_lens, lam, lambda_init, rms_w, e
     tol = np.zeros((T, H, 2 * d))
     for s in range(len(kv_lens)):
         n, L = int(cu_q[s + 1] - cu_q[s]), int(kv_lens[s])
-        k, v = np.zeros((L, Hkv, 2, d)), np.zeros((L, Hkv, 2 * d))
-        for i in range(L):
-            j = i // page
-            pg = int(table[s, j]) if j < table.shape[1] else -1
+        held = min(L, table.shape[1] * page)
+        k, v = np.zeros((held, Hkv, 2, d)), np.zeros((held, Hkv, 2 * d))
+        for i in range(held):
+            pg = int(table[s, i // page])
             if 0 <= pg < P:
                 k[i], v[i] = k_cache[pg, i % page], v_cache[pg, i % page]
         for i in range(n):
             t = int(cu_q[s]) + i
-            see = L if not causal else max(0, L - n + i + 1)
+            see = held if not causal else min(held, max(0, L - n + i + 1))
             for h in range(H):
                 g = h // (H // Hkv)
                 o, e = np.zeros(2 * d), np.zeros(2 * d)
