@@ -90,9 +90,10 @@ struct MapKey {
   uint64_t d[4];
   int kind;      // 1: uint8, 2: bf16, 4: packed e2m1
   int box_rows;
+  int box_outer = 1;  // extent of the box along d[3]
   bool operator==(const MapKey& o) const {
     return base == o.base && d[0] == o.d[0] && d[1] == o.d[1] && d[2] == o.d[2] && d[3] == o.d[3] &&
-           kind == o.kind && box_rows == o.box_rows;
+           kind == o.kind && box_rows == o.box_rows && box_outer == o.box_outer;
   }
 };
 struct MapSlot {
@@ -122,7 +123,8 @@ bool encode_uncached(CUtensorMap* m, const MapKey& k) {
   }
   const uint64_t e = static_cast<uint64_t>(k.kind);
   const cuuint64_t strides[3] = {k.d[0] * e, k.d[0] * k.d[1] * e, k.d[0] * k.d[1] * k.d[2] * e};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / e), 1, static_cast<cuuint32_t>(k.box_rows), 1};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / e), 1, static_cast<cuuint32_t>(k.box_rows),
+                             static_cast<cuuint32_t>(k.box_outer)};
   return fn(m, e == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
             const_cast<void*>(k.base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -135,7 +137,8 @@ bool encode_uncached(CUtensorMap* m, const MapKey& k) {
 size_t map_slot(const MapKey& k) {
   uint64_t h = reinterpret_cast<uintptr_t>(k.base) * 0x9E3779B97F4A7C15ull;
   for (int i = 0; i < 4; ++i) h = (h ^ k.d[i]) * 0x100000001B3ull;
-  h ^= static_cast<uint64_t>(k.kind) * 31 + static_cast<uint64_t>(k.box_rows);
+  h ^= static_cast<uint64_t>(k.kind) * 31 + static_cast<uint64_t>(k.box_rows) +
+       (static_cast<uint64_t>(k.box_outer - 1) << 16);
   return static_cast<size_t>((h >> 29) % (kMapSlots / 2)) * 2;
 }
 
@@ -160,11 +163,11 @@ bool encode_cached(CUtensorMap* m, const MapKey& k) {
 }
 
 // 4-D map over a row-major tensor with dims (innermost first) d0..d3 of bf16
-// (esize 2) or byte (esize 1) elements; box = 128 bytes x 1 x box_rows x 1,
-// 128-byte swizzle, zero fill out of bounds.
+// (esize 2) or byte (esize 1) elements; box = 128 bytes x 1 x box_rows x
+// box_outer, 128-byte swizzle, zero fill out of bounds.
 bool encode_4d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t d3,
-               int esize = 2, int box_rows = 128) {
-  return encode_cached(m, MapKey{base, {d0, d1, d2, d3}, esize, box_rows});
+               int esize = 2, int box_rows = 128, int box_outer = 1) {
+  return encode_cached(m, MapKey{base, {d0, d1, d2, d3}, esize, box_rows, box_outer});
 }
 
 // 4-D map over packed e2m1 codes, dims (innermost first) d0 codes (two per
@@ -757,6 +760,13 @@ int diffattn_extend(const void* q, const void* k_cache, const void* v_cache, con
   a.mode = mode;
   a.o = o;
   a.workspace = workspace;
+  if (extend_wide_possible(a.n)) {
+    const uint64_t slots = static_cast<uint64_t>(num_pages) * page_size, kv = static_cast<uint64_t>(H_kv);
+    const int G = H / H_kv, rows = page_size < 128 ? page_size : 128;
+    if (!encode_4d(&a.tq, q, d, 2, H, T, 2, G, 128 / G) || !encode_4d(&a.tk, k_cache, d, 2 * kv, slots, 1, 2, rows) ||
+        !encode_4d(&a.tv, v_cache, 2 * d, kv, slots, 1, 2, rows))
+      return DIFFATTN_ERR_CUDA;
+  }
   DevCtl ctl;
   if (dev_ctl(&ctl) != cudaSuccess) return DIFFATTN_ERR_CUDA;
   return cuda_status(launch_extend(a, ctl, stream));

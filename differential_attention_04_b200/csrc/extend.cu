@@ -333,6 +333,7 @@ size_t narrow_record_bytes(const ExtendShape& n) {
 }
 }  // namespace
 
+bool extend_wide_possible(const ExtendShape& n) { return wide_possible(n); }
 size_t extend_plan_bytes(const ExtendShape& n) { return plan_layout(n).bytes; }
 
 size_t extend_workspace_bytes(const ExtendShape& n) {
@@ -357,7 +358,7 @@ cudaError_t launch_extend(const ExtendArgs& a, DevCtl ctl, cudaStream_t stream) 
   if (wide && (e = launch_extend_wide(a, wrecs, ctl, stream)) != cudaSuccess) return e;
   // no item can be split where every request's keys fit one unit
   if (!wide && static_cast<long long>(a.max_pages) * a.page_size <= kUnit) return cudaSuccess;
-  const unsigned grid = kNarrowWorkers * kNarrowRows;
+  const unsigned grid = kNarrowWorkers * kNarrowRows + (wide ? kWideWorkers * kWideRows : 0);
   if (a.n.d == 128)
     extend_join_kernel<128><<<grid, kJoinThreads, 0, stream>>>(a, nrecs, wrecs, ctl.status);
   else

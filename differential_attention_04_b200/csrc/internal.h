@@ -175,7 +175,11 @@ struct ExtendArgs {
   int mode;
   void* o;
   void* workspace;
+  // wide requests only: q as (d, 2, H, T) with boxes of 64 x 1 x G x 128 / G; k_cache as
+  // (d, 2 H_kv, slots, 1) and v_cache as (2 d, H_kv, slots, 1) with boxes of 64 x 1 x min(page_size, 128) x 1
+  CUtensorMap tq, tk, tv;
 };
+bool extend_wide_possible(const ExtendShape& n);
 size_t extend_plan_bytes(const ExtendShape& n);
 size_t extend_workspace_bytes(const ExtendShape& n);
 cudaError_t launch_extend_plan(const int* cu_q, const int* kv_lens, const ExtendShape& n, int causal, void* plan,
