@@ -164,49 +164,70 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
     wpre[ntiles] = wunits;
   }
   __syncthreads();
-  const long long U[2] = {nunits, wunits * n.H_kv};
+  // an item costs its units and kNarrowCost or kWideCost more; a boundary inside those is one before its first unit
+  const long long U[2] = {nunits + static_cast<long long>(nreqs) * n.H_kv * kNarrowCost,
+                          (wunits + static_cast<long long>(ntiles) * kWideCost) * n.H_kv};
   const int W[2] = {static_cast<int>(min(U[0], static_cast<long long>(kNarrowWorkers))),
                     static_cast<int>(min(U[1], static_cast<long long>(wide_workers)))};
-  if (tid == 0) {
-    *head = PlanHeader{{U[0], U[1]}, {W[0], W[1]}, causal, ntiles, n, kPlanMagic, 0};
-  }
+  if (tid == 0) *head = PlanHeader{{W[0], W[1]}, causal, ntiles, n, kPlanMagic, {}};
   // the workers: where each begins, and the item that it leaves unfinished
   for (int i = tid; i < kNarrowWorkers + kWideWorkers; i += kPlanThreads) {
     const int c = i >= kNarrowWorkers, w = c ? i - kNarrowWorkers : i;
     WorkStart st{0, 0, 0, 0};
     WorkTail tl{0, 0, 0, 0};
     if (w < W[c]) {
-      // the item of unit u: (list index, key head), its first unit and the one behind its last
-      auto item = [&](long long u, int* hk, long long* b, long long* e) -> int {
+      const int ic = c ? kWideCost : kNarrowCost;
+      // the item at u on the line of costs, its first unit and the one behind its last (counted over all
+      // items), and the unit of it that u means
+      struct Spot {
+        int at, hk;
+        long long b, e;
+        long long unit;
+      };
+      auto spot = [&](long long u) -> Spot {
+        Spot r;
         if (c == 0) {
-          const int r = last_at_most(0, nreqs - 1, u, [&](int k) { return npre[k]; });
-          const long long per = (npre[r + 1] - npre[r]) / n.H_kv;
-          *hk = static_cast<int>((u - npre[r]) / per);
-          *b = npre[r] + *hk * per;
-          *e = *b + per;
+          auto cost = [&](int k) { return npre[k] + static_cast<long long>(k) * n.H_kv * ic; };
+          r.at = last_at_most(0, nreqs - 1, u, cost);
+          const long long per = (npre[r.at + 1] - npre[r.at]) / n.H_kv, off = u - cost(r.at);
+          r.hk = static_cast<int>(off / (per + ic));
+          r.b = npre[r.at] + r.hk * per;
+          r.e = r.b + per;
+          r.unit = max(0ll, off - r.hk * (per + ic) - ic);
           return r;
         }
-        const int any = last_at_most(0, ntiles - 1, u, [&](int k) { return wpre[wide[k].first] * n.H_kv; });
+        auto cost = [&](int k) { return wpre[k] + static_cast<long long>(k) * ic; };  // of one key head
+        const int any = last_at_most(0, ntiles - 1, u, [&](int k) { return cost(wide[k].first) * n.H_kv; });
         const int first = wide[any].first, cnt = wide[any].count;
-        const long long off = wpre[first], per = wpre[first + cnt] - off;
-        *hk = static_cast<int>((u - off * n.H_kv) / per);
-        const long long base = off * n.H_kv + *hk * per;
-        const int x = last_at_most(first, first + cnt - 1, u - base, [&](int k) { return wpre[k] - off; });
-        *b = base + wpre[x] - off;
-        *e = base + wpre[x + 1] - off;
-        return x;
+        const long long per = cost(first + cnt) - cost(first), off = u - cost(first) * n.H_kv;
+        r.hk = static_cast<int>(off / per);
+        const long long in = off - r.hk * per;
+        r.at = last_at_most(first, first + cnt - 1, in, [&](int k) { return cost(k) - cost(first); });
+        r.b = wpre[first] * n.H_kv + r.hk * (wpre[first + cnt] - wpre[first]) + wpre[r.at] - wpre[first];
+        r.e = r.b + wpre[r.at + 1] - wpre[r.at];
+        r.unit = max(0ll, in - (cost(r.at) - cost(first)) - ic);
+        return r;
       };
-      auto start_of = [&](long long v) { return v * U[c] / W[c]; };
-      const long long u0 = start_of(w), u1 = start_of(w + 1);
-      int hk;
-      long long b, e;
-      const int at = item(u0, &hk, &b, &e);
-      st = WorkStart{at, hk, static_cast<int>(u0 - b), static_cast<int>(u1 - u0)};
-      const int last = item(u1 - 1, &hk, &b, &e);
-      if (b >= u0 && e > u1) {
-        int parts = 1;
-        while (w + parts < W[c] && start_of(w + parts) < e) ++parts;
-        tl = WorkTail{last, hk, parts, 0};
+      const long long all = c ? wunits * n.H_kv : nunits;
+      // the first unit of worker v, over all items
+      auto first_of = [&](int v) -> long long {
+        if (v >= W[c]) return all;
+        const Spot x = spot(v * U[c] / W[c]);
+        return x.b + x.unit;
+      };
+      const Spot x0 = spot(w * U[c] / W[c]);
+      const long long u0 = x0.b + x0.unit, u1 = first_of(w + 1);
+      if (u1 > u0) {
+        st = WorkStart{x0.at, x0.hk, static_cast<int>(x0.unit), static_cast<int>(u1 - u0)};
+        if (w + 1 < W[c]) {
+          // the item at the range's end: unfinished if the next worker begins inside it
+          const Spot x1 = spot((w + 1) * U[c] / W[c]);
+          if (x1.unit > 0 && x1.b >= u0) {
+            int parts = 1;
+            while (first_of(w + parts) < x1.e) ++parts;
+            tl = WorkTail{x1.at, x1.hk, parts, 0};
+          }
+        }
       }
     }
     reinterpret_cast<WorkStart*>(plan + lay.starts[c])[w] = st;

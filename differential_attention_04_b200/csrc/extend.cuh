@@ -24,16 +24,16 @@ namespace diffattn {
 constexpr int kUnit = 128;
 constexpr int kNarrowRows = 8;
 constexpr int kWideRows = 128;
+constexpr int kNarrowCost = 0, kWideCost = 3;
 constexpr int kNarrowWorkers = 148;  // one CTA per SM
 constexpr int kWideWorkers = 74;     // one CTA pair per two SMs
 
 struct PlanHeader {
-  long long units[2];  // of the narrow and the wide class
-  int workers[2];      // workers with units
+  int workers[2];      // workers of the narrow and the wide class
   int causal;
   int tiles;           // entries of the list of row tiles
   ExtendShape shape;   // the sizes that the plan was made for
-  int magic, pad;
+  int magic, pad[5];
 };
 constexpr int kPlanMagic = 0x64706c6e;
 constexpr int kMaxKeys = 0x7fffff00;  // keys of a request: a unit behind the last one still has a 32-bit index
