@@ -59,9 +59,15 @@ def _launch(name: str, tensors, *args) -> None:
     device that `tensors` (every tensor the call reads or writes) live on, with
     that device current: the library launches on the current device."""
     dev = _dev(*tensors)
-    with torch.cuda.device(dev):
-        status = getattr(lib(), name)(*args, torch.cuda.current_stream(dev).cuda_stream)
-    _check(name, status)
+    fn = getattr(lib(), name)
+    # the raw getters: a Stream object and a device context cost more host time than the call itself
+    if torch._C._cuda_getDevice() == dev.index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if status != OK:
+        raise DiffAttnError(name, status)
 
 
 # Shape and dtype checks run before the device check, so that every tensor the
@@ -460,8 +466,15 @@ def diffattn_decode_noalloc(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
 
 
 # ------------------------------------------------ serving from a paged cache --
+# These calls are short and made every step, so their checks build a message only when one fails.
 def _i32(name: str, t: torch.Tensor, *shape: int) -> None:
-    _need(t.dtype == torch.int32 and tuple(t.shape) == shape, f"{name} must be int32 of shape {shape}")
+    if t.dtype is not torch.int32 or t.shape != shape:
+        raise ValueError(f"{name} must be int32 of shape {shape}")
+
+
+def _same(name: str, t: torch.Tensor, shape, dtype) -> None:
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}")
 
 
 def paged_step(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -485,14 +498,13 @@ def paged_step(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torc
     if pool_out is None:
         pool_out = pool
     _i32("pool_out", pool_out, 2)
-    if out is None:
-        new = lambda n: torch.empty(n, dtype=torch.int32, device=ctx_lens.device)
-        out = (new(S + 1), new(S), new(T), new(T), new(4))
-    _need(len(out) == 5, "out must hold (cu_q, kv_lens, positions, slots, info)")
+    if out is None:  # parts of one allocation
+        out = torch.empty(2 * S + 2 * T + 5, dtype=torch.int32, device=ctx_lens.device).split((S + 1, S, T, T, 4))
+    else:
+        _need(len(out) == 5, "out must hold (cu_q, kv_lens, positions, slots, info)")
+        for name, t, n in zip(("cu_q", "kv_lens", "positions", "slots", "info"), out, (S + 1, S, T, T, 4)):
+            _i32(name, t, n)
     cu_q, kv_lens, positions, slots, info = out
-    for name, t, n in (("cu_q", cu_q, S + 1), ("kv_lens", kv_lens, S), ("positions", positions, T),
-                       ("slots", slots, T), ("info", info, 4)):
-        _i32(name, t, n)
     _launch("diffattn_paged_step", (ctx_lens, new_lens, block_table, free_pages, pool, pool_out, *out),
             _ptr(ctx_lens), _ptr(new_lens), S, _ptr(block_table), max_pages, _ptr(free_pages), free_pages.numel(),
             _ptr(pool), _ptr(pool_out), int(page_size), T, _ptr(cu_q), _ptr(kv_lens), _ptr(positions), _ptr(slots),
@@ -541,11 +553,11 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table
         out = (torch.empty_like(q), None if k is None else torch.empty_like(k))
     _need(len(out) == 2, "out must hold (q', k')")
     qo, ko = out
-    _like("q'", qo, q.shape, q.dtype)
+    _same("q'", qo, q.shape, q.dtype)
     _need((ko is None) == (k is None), "out must hold k' exactly when k is given")
     ts = (q, positions, table, qo)
     if k is not None:
-        _like("k'", ko, k.shape, k.dtype)
+        _same("k'", ko, k.shape, k.dtype)
         ts += (k, ko)
     _launch("diffattn_rope", ts, _ptr(q), _ptr(k), _ptr(positions), _ptr(table), n_pos, T, H, H_kv, d, rot, dt,
             int(layout), int(bool(inverse)), _ptr(qo), _ptr(ko))
@@ -557,7 +569,7 @@ def _cache_shapes(k_cache, v_cache, d, dtype):
     _need(k_cache.dim() == 5 and tuple(k_cache.shape[3:]) == (2, d) and k_cache.dtype == dtype,
           "k_cache must be [num_pages, page_size, H_kv, 2, d] of q's dtype")
     P, ps, H_kv = k_cache.shape[:3]
-    _like("v_cache", v_cache, (P, ps, H_kv, 2 * d), dtype)
+    _same("v_cache", v_cache, (P, ps, H_kv, 2 * d), dtype)
     return P, ps, H_kv
 
 
@@ -570,8 +582,8 @@ def kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torc
     _need(q.dim() == 4 and q.shape[2] == 2 and q.dtype == torch.bfloat16, "q must be bfloat16 [T, H, 2, d]")
     T, H, _, d = q.shape
     num_pages, page_size, H_kv = _cache_shapes(k_cache, v_cache, d, torch.bfloat16)
-    _like("k", k, (T, H_kv, 2, d), torch.bfloat16)
-    _like("v", v, (T, H_kv, 2 * d), torch.bfloat16)
+    _same("k", k, (T, H_kv, 2, d), torch.bfloat16)
+    _same("v", v, (T, H_kv, 2 * d), torch.bfloat16)
     _i32("slots", slots, T)
     n_pos = rot = 0
     ts = (q, k, v, slots, k_cache, v_cache)
@@ -581,7 +593,7 @@ def kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torc
         ts += (positions, table)
     if out is None:
         out = torch.empty_like(q)
-    _like("out", out, q.shape, q.dtype)
+    _same("out", out, q.shape, q.dtype)
     _launch("diffattn_kv_append", ts + (out,), _ptr(q), _ptr(k), _ptr(v),
             None if table is None else _ptr(positions), _ptr(slots), _ptr(table), n_pos, T, H, H_kv, d, rot,
             int(layout), num_pages, page_size, _ptr(out), _ptr(k_cache), _ptr(v_cache))
@@ -636,10 +648,9 @@ def diffattn_extend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     _f32("rms_w", rms_w, 2 * d)
     if out is None:
         out = torch.zeros((T, H, 2 * d), dtype=q.dtype, device=q.device)
-    _like("out", out, (T, H, 2 * d), q.dtype)
-    need = extend_workspace_size(plan)
+    _same("out", out, (T, H, 2 * d), q.dtype)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(max(extend_workspace_size(plan), 16), dtype=torch.uint8, device=q.device)
     _launch("diffattn_extend", (q, k_cache, v_cache, block_table, plan.buf, lam, rms_w, workspace, out),
             _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1], num_pages, page_size,
             _ptr(plan.buf), plan.buf.numel() * plan.buf.element_size(), plan.S, T, H, H_kv, d, plan.max_new,

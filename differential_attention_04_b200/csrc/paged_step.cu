@@ -10,8 +10,9 @@
 // Nothing that the step reads is written by it (pages returned in a step are
 // free from the next one on), so no part waits for another.
 //
-// Latency-bound: a few bytes per token.  One launch: every CTA scans the
-// requests itself (2 S integers from L2, cheaper than a second launch), keeps
+// Latency-bound: a few bytes per token.  One launch (a second, of one thread,
+// only where the new pool replaces the old one in place and several CTAs read
+// it): every CTA scans the requests itself (2 S integers from L2, cheaper than a second launch), keeps
 // the prefix sums in shared memory, then takes its share of the tokens (each
 // found by binary search) and of the table entries.
 #include <cuda_runtime.h>
@@ -37,40 +38,56 @@ struct StepParams {
   int* pool_out;
   int P, T;
   int *cu_q, *kv, *pos, *slots, *info;
+  int write_pool;
 };
 
 struct Sums {
   long long tok, need, rel;
 };
 
-// Exclusive block scan of three sums; `total` gets the block's sums.
-__device__ __forceinline__ Sums block_scan(Sums v, Sums* sm, Sums& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Sums x = v;
+__device__ __forceinline__ Sums operator+(const Sums& a, const Sums& b) {
+  return Sums{a.tok + b.tok, a.need + b.need, a.rel + b.rel};
+}
+__device__ __forceinline__ Sums operator-(const Sums& a, const Sums& b) {
+  return Sums{a.tok - b.tok, a.need - b.need, a.rel - b.rel};
+}
+
+// Inclusive scan over the first `width` lanes of a warp.
+template <int WIDTH>
+__device__ __forceinline__ Sums warp_scan(Sums x, int lane) {
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const long long a = __shfl_up_sync(0xffffffffu, x.tok, off), b = __shfl_up_sync(0xffffffffu, x.need, off),
-                    c = __shfl_up_sync(0xffffffffu, x.rel, off);
-    if (lane >= off) {
-      x.tok += a;
-      x.need += b;
-      x.rel += c;
-    }
+  for (int off = 1; off < WIDTH; off <<= 1) {
+    const Sums o{__shfl_up_sync(0xffffffffu, x.tok, off), __shfl_up_sync(0xffffffffu, x.need, off),
+                 __shfl_up_sync(0xffffffffu, x.rel, off)};
+    if (lane >= off) x = x + o;
   }
+  return x;
+}
+
+// Exclusive block scan; `total` gets the block's sums.  The warps' totals are
+// scanned by every warp for itself.
+__device__ __forceinline__ Sums block_scan(Sums v, Sums* sm, Sums& total) {
+  constexpr int kWarps = kStepThreads / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Sums x = warp_scan<32>(v, lane);
   if (lane == 31) sm[warp] = x;
   __syncthreads();
-  Sums before{0, 0, 0};
-  total = Sums{0, 0, 0};
-#pragma unroll
-  for (int w = 0; w < kStepThreads / 32; ++w) {
-    if (w == warp) before = total;
-    total.tok += sm[w].tok;
-    total.need += sm[w].need;
-    total.rel += sm[w].rel;
-  }
-  __syncthreads();  // sm is reused
-  return Sums{before.tok + x.tok - v.tok, before.need + x.need - v.need, before.rel + x.rel - v.rel};
+  const Sums w = warp_scan<kWarps>(sm[lane & (kWarps - 1)], lane);
+  auto of = [&](const Sums& s, int from) {
+    return Sums{__shfl_sync(0xffffffffu, s.tok, from), __shfl_sync(0xffffffffu, s.need, from),
+                __shfl_sync(0xffffffffu, s.rel, from)};
+  };
+  total = of(w, kWarps - 1);
+  const Sums before = of(w, max(warp - 1, 0));
+  return (warp ? before + x : x) - v;
 }
+
+// ceil(tokens / P); tokens and P are at most 2^31 - 1, so the sum fits 32 bits unsigned.
+__device__ __forceinline__ int pages_of(int tokens, int P) {
+  return static_cast<int>((static_cast<unsigned>(tokens) + static_cast<unsigned>(P) - 1u) / static_cast<unsigned>(P));
+}
+// at mod F for at < 2 F.
+__device__ __forceinline__ unsigned in_ring(unsigned at, unsigned F) { return at >= F ? at - F : at; }
 
 __global__ void __launch_bounds__(kStepThreads) paged_step_kernel(const StepParams p) {
   extern __shared__ int sm_dyn[];
@@ -82,42 +99,41 @@ __global__ void __launch_bounds__(kStepThreads) paged_step_kernel(const StepPara
   const int tid = threadIdx.x;
   if (tid == 0) s_bad = 0;
   __syncthreads();
-  // Every request's needs; sums in 64 bits, and a step whose sums do not fit
-  // 32 bits fails the checks below before any of them is used.
-  Sums carry{0, 0, 0};
-  int bad = 0;
-  for (int base = 0; base < p.S; base += kStepThreads) {
-    const int s = base + tid;
-    Sums v{0, 0, 0};
-    if (s < p.S) {
-      const int c = p.ctx[s], n = p.nlen[s];
-      if (c < 0 || n < -1 || static_cast<long long>(c) + n > 0x7fffffffll) {
-        bad |= 8;
-      } else {
-        const int old = static_cast<int>((static_cast<long long>(c) + p.P - 1) / p.P);
-        if (old > p.max_pages) bad |= 2;
-        if (n < 0) {
-          v.rel = old;
-        } else {
-          const int want = static_cast<int>((static_cast<long long>(c) + n + p.P - 1) / p.P);
-          if (want > p.max_pages) bad |= 2;
-          v.tok = n;
-          v.need = want - old;
-        }
-      }
-    }
-    Sums total;
-    const Sums at = block_scan(v, warp_sums, total);
-    if (s < p.S) {
-      tok0[s] = static_cast<int>(carry.tok + at.tok);
-      need0[s] = static_cast<int>(carry.need + at.need);
-      rel0[s] = static_cast<int>(carry.rel + at.rel);
-    }
-    carry.tok += total.tok;
-    carry.need += total.need;
-    carry.rel += total.rel;
-  }
   const int head = p.pool[0], count = p.pool[1];
+  // Every request's needs, a run of requests per thread; sums in 64 bits, and a
+  // step whose sums do not fit 32 bits fails the checks below before any of
+  // them is used.
+  const int per = (p.S + kStepThreads - 1) / kStepThreads;
+  const int s_lo = min(tid * per, p.S), s_hi = min(s_lo + per, p.S);
+  int bad = 0;
+  auto needs = [&](int s) {
+    Sums v{0, 0, 0};
+    const int c = p.ctx[s], n = p.nlen[s];
+    if (c < 0 || n < -1 || static_cast<long long>(c) + n > 0x7fffffffll) {
+      bad |= 8;
+      return v;
+    }
+    const int old = pages_of(c, p.P);
+    if (old > p.max_pages) bad |= 2;
+    if (n < 0) {
+      v.rel = old;
+    } else {
+      const int want = pages_of(c + n, p.P);
+      if (want > p.max_pages) bad |= 2;
+      v.tok = n;
+      v.need = want - old;
+    }
+    return v;
+  };
+  Sums mine{0, 0, 0}, carry;
+  for (int s = s_lo; s < s_hi; ++s) mine = mine + needs(s);
+  Sums at = block_scan(mine, warp_sums, carry);
+  for (int s = s_lo; s < s_hi; ++s) {
+    tok0[s] = static_cast<int>(at.tok);
+    need0[s] = static_cast<int>(at.need);
+    rel0[s] = static_cast<int>(at.rel);
+    at = at + needs(s);
+  }
   if (tid == 0) {
     if (carry.need > count) bad |= 1;
     if (carry.tok > p.T) bad |= 4;
@@ -136,8 +152,12 @@ __global__ void __launch_bounds__(kStepThreads) paged_step_kernel(const StepPara
     p.info[1] = static_cast<int>(min(carry.need, 0x7fffffffll));
     p.info[2] = static_cast<int>(min(carry.rel, 0x7fffffffll));
     p.info[3] = status;
-    // pool and pool_out may be one buffer, and other CTAs may still have to
-    // read it: the launch with one CTA writes it here, else a second kernel
+    // Where pool and pool_out share words, other CTAs may still have to read
+    // them: then a second kernel writes the result.
+    if (p.write_pool) {
+      p.pool_out[0] = ok ? static_cast<int>((head + carry.need) % p.F) : head;
+      p.pool_out[1] = ok ? static_cast<int>(count - carry.need + carry.rel) : count;
+    }
   }
   // the requests' offsets and lengths
   for (int s = gtid; s <= p.S; s += gsize) {
@@ -147,39 +167,42 @@ __global__ void __launch_bounds__(kStepThreads) paged_step_kernel(const StepPara
       p.kv[s] = ok && n >= 0 ? p.ctx[s] + n : 0;
     }
   }
-  // pages: one request per warp
+  // the request of entry e: the last one whose entries begin at or before it
+  auto owner = [&](const int* first, int e) {
+    int lo = 0, hi = p.S - 1;
+    while (lo < hi) {
+      const int m = (lo + hi + 1) >> 1;
+      if (first[m] <= e) lo = m;
+      else hi = m - 1;
+    }
+    return lo;
+  };
+  // pages, an entry a thread: a finished request may return thousands, and a
+  // warp that walked its row alone would take a trip to memory per 32 of them
+  // (14.7 us against 6.5 us in all for 700 requests of up to 32K tokens)
   if (ok) {
-    const int lane = tid & 31;
-    for (int s = gtid >> 5; s < p.S; s += gsize >> 5) {
-      const int c = p.ctx[s], n = p.nlen[s];
-      const int old = static_cast<int>((static_cast<long long>(c) + p.P - 1) / p.P);
-      int* row = p.bt + static_cast<size_t>(s) * p.max_pages;
-      if (n < 0) {
-        for (int j = lane; j < old; j += 32)
-          p.ring[(static_cast<long long>(head) + count + rel0[s] + j) % p.F] = row[j];
-      } else {
-        const int want = static_cast<int>((static_cast<long long>(c) + n + p.P - 1) / p.P);
-        for (int j = old + lane; j < want; j += 32)
-          row[j] = p.ring[(static_cast<long long>(head) + need0[s] + j - old) % p.F];
-      }
+    const int taken = static_cast<int>(carry.need), back = static_cast<int>(carry.rel);
+    for (int e = gtid; e < back; e += gsize) {
+      const int s = owner(rel0, e);
+      p.ring[in_ring(static_cast<unsigned>(head) + count + e, p.F)] =
+          p.bt[static_cast<size_t>(s) * p.max_pages + (e - rel0[s])];
+    }
+    for (int e = gtid; e < taken; e += gsize) {
+      const int s = owner(need0, e);
+      p.bt[static_cast<size_t>(s) * p.max_pages + pages_of(p.ctx[s], p.P) + (e - need0[s])] =
+          p.ring[in_ring(static_cast<unsigned>(head) + e, p.F)];
     }
   }
   // tokens: a page that was there before comes from the table, a new one from the ring
   for (int t = gtid; t < p.T; t += gsize) {
     int pos = -1, slot = -1;
     if (t < total) {
-      int lo = 0, hi = p.S - 1;  // the last request with tok0 <= t
-      while (lo < hi) {
-        const int m = (lo + hi + 1) >> 1;
-        if (tok0[m] <= t) lo = m;
-        else hi = m - 1;
-      }
+      const int lo = owner(tok0, t);
       const int c = p.ctx[lo];
       pos = c + t - tok0[lo];
-      const int old = static_cast<int>((static_cast<long long>(c) + p.P - 1) / p.P);
-      const int j = pos / p.P;
+      const int old = pages_of(c, p.P), j = pos / p.P;
       const int page = j < old ? p.bt[static_cast<size_t>(lo) * p.max_pages + j]
-                               : p.ring[(static_cast<long long>(head) + need0[lo] + j - old) % p.F];
+                               : p.ring[in_ring(static_cast<unsigned>(head) + need0[lo] + (j - old), p.F)];
       // a page number that is no page's stays out of every cache's range
       slot = page < 0 ? -1 : static_cast<int>(min(static_cast<long long>(page) * p.P + pos % p.P, 0x7fffffffll));
     }
@@ -202,7 +225,7 @@ cudaError_t launch_paged_step(const int* ctx_lens, const int* new_lens, int S, i
                               int* free_pages, int ring_size, const int* pool, int* pool_out, int page_size, int T,
                               int* cu_q, int* kv_lens, int* positions, int* slots, int* info, cudaStream_t stream) {
   StepParams p = {ctx_lens, new_lens, S,    block_table, max_pages, free_pages, ring_size, pool,
-                  pool_out, page_size, T,   cu_q,        kv_lens,   positions,  slots,     info};
+                  pool_out, page_size, T,   cu_q,        kv_lens,   positions,  slots,     info,       0};
   const size_t smem = static_cast<size_t>(3 * S + 1) * sizeof(int);
   cudaError_t e = cudaSuccess;
   if (smem > 48 * 1024) {
@@ -213,9 +236,11 @@ cudaError_t launch_paged_step(const int* ctx_lens, const int* new_lens, int S, i
   const int work = T > S * 32 ? T : S * 32;
   int grid = (work + kStepThreads - 1) / kStepThreads;
   if (grid > 148) grid = 148;
+  const bool apart = pool_out + 2 <= pool || pool + 2 <= pool_out;
+  p.write_pool = grid == 1 || apart;
   paged_step_kernel<<<grid, kStepThreads, smem, stream>>>(p);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.write_pool) return e;
   paged_step_pool_kernel<<<1, 1, 0, stream>>>(pool, ring_size, info, pool_out);
   return cudaGetLastError();
 }
