@@ -499,7 +499,8 @@ def paged_step(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torc
         pool_out = pool
     _i32("pool_out", pool_out, 2)
     if out is None:  # parts of one allocation
-        out = torch.empty(2 * S + 2 * T + 5, dtype=torch.int32, device=ctx_lens.device).split((S + 1, S, T, T, 4))
+        out = torch.unsafe_split_with_sizes(
+            torch.empty(2 * S + 2 * T + 5, dtype=torch.int32, device=ctx_lens.device), (S + 1, S, T, T, 4))
     else:
         _need(len(out) == 5, "out must hold (cu_q, kv_lens, positions, slots, info)")
         for name, t, n in zip(("cu_q", "kv_lens", "positions", "slots", "info"), out, (S + 1, S, T, T, 4)):

@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
       // items), and the unit of it that u means
       struct Spot {
         int at, hk;
-        long long b, e;
+        long long cost, b, e;  // where the item begins on the line; its first unit and the one behind its last
         long long unit;
       };
       auto spot = [&](long long u) -> Spot {
@@ -191,43 +191,37 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
           r.at = last_at_most(0, nreqs - 1, u, cost);
           const long long per = (npre[r.at + 1] - npre[r.at]) / n.H_kv, off = u - cost(r.at);
           r.hk = static_cast<int>(off / (per + ic));
+          r.cost = cost(r.at) + r.hk * (per + ic);
           r.b = npre[r.at] + r.hk * per;
           r.e = r.b + per;
-          r.unit = max(0ll, off - r.hk * (per + ic) - ic);
-          return r;
+        } else {
+          auto cost = [&](int k) { return wpre[k] + static_cast<long long>(k) * ic; };  // of one key head
+          const int any = last_at_most(0, ntiles - 1, u, [&](int k) { return cost(wide[k].first) * n.H_kv; });
+          const int first = wide[any].first, cnt = wide[any].count;
+          const long long c0 = cost(first), per = cost(first + cnt) - c0, off = u - c0 * n.H_kv;
+          r.hk = static_cast<int>(off / per);
+          const long long in = off - r.hk * per;
+          r.at = last_at_most(first, first + cnt - 1, in, [&](int k) { return cost(k) - c0; });
+          r.cost = c0 * n.H_kv + r.hk * per + cost(r.at) - c0;
+          r.b = wpre[first] * n.H_kv + r.hk * (wpre[first + cnt] - wpre[first]) + wpre[r.at] - wpre[first];
+          r.e = r.b + wpre[r.at + 1] - wpre[r.at];
         }
-        auto cost = [&](int k) { return wpre[k] + static_cast<long long>(k) * ic; };  // of one key head
-        const int any = last_at_most(0, ntiles - 1, u, [&](int k) { return cost(wide[k].first) * n.H_kv; });
-        const int first = wide[any].first, cnt = wide[any].count;
-        const long long per = cost(first + cnt) - cost(first), off = u - cost(first) * n.H_kv;
-        r.hk = static_cast<int>(off / per);
-        const long long in = off - r.hk * per;
-        r.at = last_at_most(first, first + cnt - 1, in, [&](int k) { return cost(k) - cost(first); });
-        r.b = wpre[first] * n.H_kv + r.hk * (wpre[first + cnt] - wpre[first]) + wpre[r.at] - wpre[first];
-        r.e = r.b + wpre[r.at + 1] - wpre[r.at];
-        r.unit = max(0ll, in - (cost(r.at) - cost(first)) - ic);
+        r.unit = max(0ll, u - r.cost - ic);
         return r;
       };
-      const long long all = c ? wunits * n.H_kv : nunits;
-      // the first unit of worker v, over all items
-      auto first_of = [&](int v) -> long long {
-        if (v >= W[c]) return all;
-        const Spot x = spot(v * U[c] / W[c]);
-        return x.b + x.unit;
-      };
       const Spot x0 = spot(w * U[c] / W[c]);
-      const long long u0 = x0.b + x0.unit, u1 = first_of(w + 1);
-      if (u1 > u0) {
-        st = WorkStart{x0.at, x0.hk, static_cast<int>(x0.unit), static_cast<int>(u1 - u0)};
-        if (w + 1 < W[c]) {
-          // the item at the range's end: unfinished if the next worker begins inside it
-          const Spot x1 = spot((w + 1) * U[c] / W[c]);
-          if (x1.unit > 0 && x1.b >= u0) {
-            int parts = 1;
-            while (first_of(w + parts) < x1.e) ++parts;
-            tl = WorkTail{x1.at, x1.hk, parts, 0};
-          }
-        }
+      const bool last = w + 1 == W[c];
+      const Spot x1 = last ? x0 : spot((w + 1) * U[c] / W[c]);
+      const long long u0 = x0.b + x0.unit, u1 = last ? (c ? wunits * n.H_kv : nunits) : x1.b + x1.unit;
+      if (u1 > u0) st = WorkStart{x0.at, x0.hk, static_cast<int>(x0.unit), static_cast<int>(u1 - u0)};
+      // The item that the range ends in is split if the next worker begins
+      // inside it (floor(v U / W) < x holds for v up to (x W - 1) / U).  Its
+      // owner is the last worker that begins at or before its first unit.
+      if (!last && x1.unit > 0) {
+        const int owner = static_cast<int>(((x1.cost + ic + 1) * W[c] - 1) / U[c]);
+        const int end = static_cast<int>(min(static_cast<long long>(W[c] - 1),
+                                             ((x1.cost + ic + x1.e - x1.b) * W[c] - 1) / U[c]));
+        if (end > w) tl = WorkTail{x1.at, x1.hk, end - owner + 1, w - owner};
       }
     }
     reinterpret_cast<WorkStart*>(plan + lay.starts[c])[w] = st;
@@ -235,117 +229,165 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
   }
 }
 
-// Joins the rows that were split: block (worker, row) adds the parts of the
-// item that the worker began, each taken to the common maximum, in the order
-// of the keys within eight groups of parts and then group by group; then the
-// epilogue of a whole row.  Reads 16 d bytes a part and row.
+// Joins the rows that were split.  An item of P parts is joined by the blocks
+// of the workers that have nothing but it at the end of their range (its owner
+// and all but the last of the others): a warp a row where there are few parts,
+// a block a row where there are many.  The parts are taken to the common
+// maximum and added in the order of the keys (many parts: within eight groups,
+// then group by group), then comes the epilogue of a whole row.  Reads 16 d
+// bytes a part and row; with one block a row for every worker it took 48 us
+// where this takes JOIN_US (a mixed step of 20 over 4 heads, d 128).
 constexpr int kJoinThreads = 256;
-constexpr int kJoinGroups = kJoinThreads / 32;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinFew = kJoinWarps;  // parts up to which a warp takes a row alone
+constexpr int kJoinWideBlocks = kWideRows / kJoinWarps;  // blocks of a wide worker (a narrow one has one)
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) extend_join_kernel(const ExtendArgs a, const float* nrecs,
                                                                    const float* wrecs, int* status) {
   constexpr int DV = 2 * D;
+  constexpr int NV = 2 * DV / 128;  // float4 of a lane: first map 1's channels, then the same of map 2
   if (!plan_fits(a.plan, a.n, status)) return;
-  const bool is_wide = blockIdx.x >= kNarrowWorkers * kNarrowRows;
-  const int bi = is_wide ? blockIdx.x - kNarrowWorkers * kNarrowRows : blockIdx.x;
-  const int rows = is_wide ? kWideRows : kNarrowRows;
-  const int w = bi / rows, r = bi % rows;
+  const bool is_wide = blockIdx.x >= kNarrowWorkers;
+  const int bi = is_wide ? blockIdx.x - kNarrowWorkers : blockIdx.x;
+  const int blocks = is_wide ? kJoinWideBlocks : 1;
+  const int w = bi / blocks;
   const PlanView pv = plan_view(a.plan, a.n, is_wide);
   const WorkTail tl = pv.tails[w];
   if (tl.parts == 0) return;
   const int G = a.n.H / a.n.H_kv;
   const int tok0 = is_wide ? pv.wide[tl.at].tok0 : pv.narrow[tl.at].q0;
-  const int ntok = is_wide ? pv.wide[tl.at].ntok : pv.narrow[tl.at].n;
-  if (r >= ntok * G) return;
+  const int R = (is_wide ? pv.wide[tl.at].ntok : pv.narrow[tl.at].n) * G;
+  const int rows = is_wide ? kWideRows : kNarrowRows;
   const float* recs = is_wide ? wrecs : nrecs;
   const size_t rec = record_floats(rows, D);
-  const int tid = threadIdx.x, lane = tid & 31, grp = tid >> 5;
-  // part p of worker w's item: its own last record, then the first records of the workers behind it
-  auto part = [&](int p) { return recs + (p == 0 ? 2 * w + 1 : 2 * (w + p)) * rec; };
-
-  __shared__ float2 f[kNarrowWorkers];  // factors of a part's two maps
-  __shared__ float red[4][kJoinGroups];
-  __shared__ float acc[kJoinGroups][2 * DV];
-  static_assert(kNarrowWorkers <= kJoinThreads, "one thread per part");
-  float4 ml = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-  if (tid < tl.parts) ml = *reinterpret_cast<const float4*>(part(tid) + 4 * r);
-  float M1 = ml.x, M2 = ml.z;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int owner = w - tl.member, team = tl.member * blocks + bi % blocks, teams = (tl.parts - 1) * blocks;
+  // part p: the owner's last record, then the first records of the workers behind it
+  auto part = [&](int p) { return recs + (p == 0 ? 2 * owner + 1 : 2 * (owner + p)) * rec; };
+  auto max_of = [](float x) {
 #pragma unroll
-  for (int off = 16; off; off >>= 1) {
-    M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, off));
-    M2 = fmaxf(M2, __shfl_xor_sync(0xffffffffu, M2, off));
-  }
-  if (lane == 0) {
-    red[0][grp] = M1;
-    red[1][grp] = M2;
-  }
-  __syncthreads();
+    for (int off = 16; off; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+    return x;
+  };
+  auto sum_of = [](float x) {
 #pragma unroll
-  for (int g = 0; g < kJoinGroups; ++g) {
-    M1 = fmaxf(M1, red[0][g]);
-    M2 = fmaxf(M2, red[1][g]);
-  }
-  const float f1 = M1 == -INFINITY ? 0.f : fast_exp2(ml.x - M1), f2 = M2 == -INFINITY ? 0.f : fast_exp2(ml.z - M2);
-  if (tid < tl.parts) f[tid] = make_float2(f1, f2);
-  float l1 = f1 * ml.y, l2 = f2 * ml.w;
-#pragma unroll
-  for (int off = 16; off; off >>= 1) {
-    l1 += __shfl_xor_sync(0xffffffffu, l1, off);
-    l2 += __shfl_xor_sync(0xffffffffu, l2, off);
-  }
-  if (lane == 0) {
-    red[2][grp] = l1;
-    red[3][grp] = l2;
-  }
-  __syncthreads();
-  constexpr int NV = 2 * DV / 128;  // float4 per lane: both maps' channels
+    for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+  };
+  const float c2 = map2_coefficient(a.mode, *a.lambda);
+  auto out_row = [&](int r) {
+    return static_cast<__nv_bfloat16*>(a.o) +
+           (static_cast<size_t>(tok0 + r / G) * a.n.H + static_cast<size_t>(tl.hk) * G + r % G) * DV;
+  };
   float4 x[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-  for (int p = grp; p < tl.parts; p += kJoinGroups) {
-    const float2 fp = f[p];
+  auto add_part = [&](int p, int r, float f1, float f2) {
     const float4* o = reinterpret_cast<const float4*>(part(p) + 4 * rows + static_cast<size_t>(r) * 2 * DV);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const float4 v = __ldg(o + 32 * i + lane);
-      const float fi = i < NV / 2 ? fp.x : fp.y;
-      x[i].x = fmaf(fi, v.x, x[i].x);
-      x[i].y = fmaf(fi, v.y, x[i].y);
-      x[i].z = fmaf(fi, v.z, x[i].z);
-      x[i].w = fmaf(fi, v.w, x[i].w);
+      const float f = i < NV / 2 ? f1 : f2;
+      x[i].x = fmaf(f, v.x, x[i].x);
+      x[i].y = fmaf(f, v.y, x[i].y);
+      x[i].z = fmaf(f, v.z, x[i].z);
+      x[i].w = fmaf(f, v.w, x[i].w);
     }
-  }
+  };
+
+  if (tl.parts <= kJoinFew) {
+    for (int r = team * kJoinWarps + warp; r < R; r += teams * kJoinWarps) {
+      float4 ml = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+      if (lane < tl.parts) ml = *reinterpret_cast<const float4*>(part(lane) + 4 * r);
+      const float M1 = max_of(ml.x), M2 = max_of(ml.z);
+      const float f1 = M1 == -INFINITY ? 0.f : fast_exp2(ml.x - M1), f2 = M2 == -INFINITY ? 0.f : fast_exp2(ml.z - M2);
+      const float l1 = sum_of(f1 * ml.y), l2 = sum_of(f2 * ml.w);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) *reinterpret_cast<float4*>(&acc[grp][4 * (32 * i + lane)]) = x[i];
-  __syncthreads();
-  float y = 0.f;
-  if (tid < DV) {
-    float o1 = 0.f, o2 = 0.f;
-    l1 = l2 = 0.f;
+      for (int i = 0; i < NV; ++i) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+      for (int p = 0; p < tl.parts; ++p)
+        add_part(p, r, __shfl_sync(0xffffffffu, f1, p), __shfl_sync(0xffffffffu, f2, p));
+      const float i1 = l1 > 0.f ? 1.f / l1 : 0.f, i2 = l2 > 0.f ? c2 / l2 : 0.f;
+      float ss = 0.f;
 #pragma unroll
-    for (int g = 0; g < kJoinGroups; ++g) {
-      o1 += acc[g][tid];
-      o2 += acc[g][DV + tid];
-      l1 += red[2][g];
-      l2 += red[3][g];
+      for (int i = 0; i < NV / 2; ++i) {
+        float4& y = x[i];
+        const float4& z = x[i + NV / 2];
+        y.x = fmaf(y.x, i1, z.x * i2);
+        y.y = fmaf(y.y, i1, z.y * i2);
+        y.z = fmaf(y.z, i1, z.z * i2);
+        y.w = fmaf(y.w, i1, z.w * i2);
+        ss += y.x * y.x + y.y * y.y + y.z * y.z + y.w * y.w;
+      }
+      const float gsc = (1.f - a.lambda_init) * rsqrtf(sum_of(ss) / DV + a.eps);
+      __nv_bfloat16* o = out_row(r);
+#pragma unroll
+      for (int i = 0; i < NV / 2; ++i) {
+        const int ch = 128 * i + 4 * lane;
+        const float* rw = a.rms_w + ch;
+        *reinterpret_cast<uint2*>(o + ch) = make_uint2(pack_bf16x2(x[i].x * gsc * rw[0], x[i].y * gsc * rw[1]),
+                                                       pack_bf16x2(x[i].z * gsc * rw[2], x[i].w * gsc * rw[3]));
+      }
     }
-    y = (l1 > 0.f ? o1 / l1 : 0.f) + map2_coefficient(a.mode, *a.lambda) * (l2 > 0.f ? o2 / l2 : 0.f);
+    return;
   }
-  float ss = y * y;
+
+  __shared__ float2 f[kNarrowWorkers];  // factors of a part's two maps
+  __shared__ float red[4][kJoinWarps];
+  __shared__ float acc[kJoinWarps][2 * DV];
+  static_assert(kNarrowWorkers <= kJoinThreads, "one thread per part");
+  for (int r = team; r < R; r += teams) {
+    float4 ml = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+    if (tid < tl.parts) ml = *reinterpret_cast<const float4*>(part(tid) + 4 * r);
+    float M1 = max_of(ml.x), M2 = max_of(ml.z);
+    if (lane == 0) {
+      red[0][warp] = M1;
+      red[1][warp] = M2;
+    }
+    __syncthreads();
 #pragma unroll
-  for (int off = 16; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-  __syncthreads();
-  if (lane == 0) red[0][grp] = ss;
-  __syncthreads();
-  ss = 0.f;
+    for (int g = 0; g < kJoinWarps; ++g) {
+      M1 = fmaxf(M1, red[0][g]);
+      M2 = fmaxf(M2, red[1][g]);
+    }
+    const float f1 = M1 == -INFINITY ? 0.f : fast_exp2(ml.x - M1), f2 = M2 == -INFINITY ? 0.f : fast_exp2(ml.z - M2);
+    if (tid < tl.parts) f[tid] = make_float2(f1, f2);
+    float l1 = sum_of(f1 * ml.y), l2 = sum_of(f2 * ml.w);
+    if (lane == 0) {
+      red[2][warp] = l1;
+      red[3][warp] = l2;
+    }
+    __syncthreads();
 #pragma unroll
-  for (int g = 0; g < kJoinGroups; ++g) ss += red[0][g];
-  if (tid < DV) {
-    const float gsc = (1.f - a.lambda_init) * rsqrtf(ss / DV + a.eps);
-    const size_t row = static_cast<size_t>(tok0 + r / G) * a.n.H + static_cast<size_t>(tl.hk) * G + r % G;
-    static_cast<__nv_bfloat16*>(a.o)[row * DV + tid] = __float2bfloat16_rn(y * gsc * a.rms_w[tid]);
+    for (int i = 0; i < NV; ++i) x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int p = warp; p < tl.parts; p += kJoinWarps) add_part(p, r, f[p].x, f[p].y);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) *reinterpret_cast<float4*>(&acc[warp][4 * (32 * i + lane)]) = x[i];
+    __syncthreads();
+    float y = 0.f;
+    if (tid < DV) {
+      float o1 = 0.f, o2 = 0.f;
+      l1 = l2 = 0.f;
+#pragma unroll
+      for (int g = 0; g < kJoinWarps; ++g) {
+        o1 += acc[g][tid];
+        o2 += acc[g][DV + tid];
+        l1 += red[2][g];
+        l2 += red[3][g];
+      }
+      y = (l1 > 0.f ? o1 / l1 : 0.f) + c2 * (l2 > 0.f ? o2 / l2 : 0.f);
+    }
+    const float part_ss = sum_of(y * y);
+    if (lane == 0) red[0][warp] = part_ss;
+    __syncthreads();
+    float ss = 0.f;
+#pragma unroll
+    for (int g = 0; g < kJoinWarps; ++g) ss += red[0][g];
+    if (tid < DV) {
+      const float gsc = (1.f - a.lambda_init) * rsqrtf(ss / DV + a.eps);
+      out_row(r)[tid] = __float2bfloat16_rn(y * gsc * a.rms_w[tid]);
+    }
+    __syncthreads();  // the next row reuses the shared memory
   }
 }
 
@@ -379,7 +421,7 @@ cudaError_t launch_extend(const ExtendArgs& a, DevCtl ctl, cudaStream_t stream) 
   if (wide && (e = launch_extend_wide(a, wrecs, ctl, stream)) != cudaSuccess) return e;
   // no item can be split where every request's keys fit one unit
   if (!wide && static_cast<long long>(a.max_pages) * a.page_size <= kUnit) return cudaSuccess;
-  const unsigned grid = kNarrowWorkers * kNarrowRows + (wide ? kWideWorkers * kWideRows : 0);
+  const unsigned grid = kNarrowWorkers + (wide ? kWideWorkers * kJoinWideBlocks : 0);
   if (a.n.d == 128)
     extend_join_kernel<128><<<grid, kJoinThreads, 0, stream>>>(a, nrecs, wrecs, ctl.status);
   else

@@ -49,12 +49,13 @@ struct WideTile {
   int L, s, first, count;  // cached tokens, request; the request's first row tile and their number
 };
 // Where a worker begins: item (at, hk), its unit, and how many units it takes.
-// Its tail: the item (at, hk) that it began and did not finish, and in how many parts (0: none).
+// Its tail: the split item (at, hk) that its range ends in and that goes on
+// behind it, in how many parts (0: there is none), and which of them it has.
 struct WorkStart {
   int at, hk, unit, count;
 };
 struct WorkTail {
-  int at, hk, parts, pad;
+  int at, hk, parts, member;
 };
 
 struct PlanLayout {
