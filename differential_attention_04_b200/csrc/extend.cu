@@ -8,8 +8,7 @@
 // (1 - lambda_init) scale (Eq. 3).
 #include <math.h>
 
-#include "common.cuh"
-#include "extend.cuh"
+#include "extend_wide.cuh"
 
 namespace diffattn {
 
@@ -74,7 +73,7 @@ __device__ __forceinline__ int last_at_most(int lo, int hi, long long u, F pre) 
 // it once for all layers.
 __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __restrict__ cu,
                                                                    const int* __restrict__ kvl, ExtendShape n,
-                                                                   int causal, int wide_workers, char* plan,
+                                                                   int causal, char* plan,
                                                                    int* status) {
   __shared__ PlanSums sm[kPlanThreads / 32];
   const PlanLayout lay = plan_layout(n);
@@ -164,19 +163,19 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
     wpre[ntiles] = wunits;
   }
   __syncthreads();
-  // an item costs its units and kNarrowCost or kWideCost more; a boundary inside those is one before its first unit
+  // an item costs its units and kNarrowCost or wide_cost(n.d) more; a boundary inside those is one before its first unit
   const long long U[2] = {nunits + static_cast<long long>(nreqs) * n.H_kv * kNarrowCost,
-                          (wunits + static_cast<long long>(ntiles) * kWideCost) * n.H_kv};
+                          (wunits + static_cast<long long>(ntiles) * wide_cost(n.d)) * n.H_kv};
   const int W[2] = {static_cast<int>(min(U[0], static_cast<long long>(kNarrowWorkers))),
-                    static_cast<int>(min(U[1], static_cast<long long>(wide_workers)))};
+                    static_cast<int>(min(U[1], static_cast<long long>(wide_workers(n.d))))};
   if (tid == 0) *head = PlanHeader{{W[0], W[1]}, causal, ntiles, n, kPlanMagic, {}};
   // the workers: where each begins, and the item that it leaves unfinished
-  for (int i = tid; i < kNarrowWorkers + kWideWorkers; i += kPlanThreads) {
+  for (int i = tid; i < kNarrowWorkers + wide_workers(n.d); i += kPlanThreads) {
     const int c = i >= kNarrowWorkers, w = c ? i - kNarrowWorkers : i;
     WorkStart st{0, 0, 0, 0};
     WorkTail tl{0, 0, 0, 0};
     if (w < W[c]) {
-      const int ic = c ? kWideCost : kNarrowCost;
+      const int ic = c ? wide_cost(n.d) : kNarrowCost;
       // the item at u on the line of costs, its first unit and the one behind its last (counted over all
       // items), and the unit of it that u means
       struct Spot {
@@ -401,14 +400,13 @@ size_t extend_plan_bytes(const ExtendShape& n) { return plan_layout(n).bytes; }
 
 size_t extend_workspace_bytes(const ExtendShape& n) {
   size_t b = narrow_record_bytes(n);
-  if (wide_possible(n)) b += 2 * kWideWorkers * record_floats(kWideRows, n.d) * sizeof(float);
+  if (wide_possible(n)) b += 2 * wide_workers(n.d) * record_floats(kWideRows, n.d) * sizeof(float);
   return b;
 }
 
 cudaError_t launch_extend_plan(const int* cu_q, const int* kv_lens, const ExtendShape& n, int causal, void* plan,
                                DevCtl ctl, cudaStream_t stream) {
-  extend_plan_kernel<<<1, kPlanThreads, 0, stream>>>(cu_q, kv_lens, n, causal ? 1 : 0, kWideWorkers,
-                                                     static_cast<char*>(plan), ctl.status);
+  extend_plan_kernel<<<1, kPlanThreads, 0, stream>>>(cu_q, kv_lens, n, causal ? 1 : 0, static_cast<char*>(plan), ctl.status);
   return cudaGetLastError();
 }
 
@@ -418,10 +416,11 @@ cudaError_t launch_extend(const ExtendArgs& a, DevCtl ctl, cudaStream_t stream) 
   const bool wide = wide_possible(a.n);
   cudaError_t e = launch_extend_narrow(a, nrecs, ctl, stream);
   if (e != cudaSuccess) return e;
-  if (wide && (e = launch_extend_wide(a, wrecs, ctl, stream)) != cudaSuccess) return e;
+  if (wide) e = a.n.d == 64 ? launch_extend_wide64(a, wrecs, ctl, stream) : launch_extend_wide128(a, wrecs, ctl, stream);
+  if (e != cudaSuccess) return e;
   // no item can be split where every request's keys fit one unit
   if (!wide && static_cast<long long>(a.max_pages) * a.page_size <= kUnit) return cudaSuccess;
-  const unsigned grid = kNarrowWorkers + (wide ? kWideWorkers * kJoinWideBlocks : 0);
+  const unsigned grid = kNarrowWorkers + (wide ? wide_workers(a.n.d) * kJoinWideBlocks : 0);
   if (a.n.d == 128)
     extend_join_kernel<128><<<grid, kJoinThreads, 0, stream>>>(a, nrecs, wrecs, ctl.status);
   else

@@ -3,7 +3,7 @@
 //
 // A request's query rows are its new tokens times the G = H / H_kv query heads
 // that share a key head.  Requests of at most kNarrowRows rows are "narrow"
-// (extend_narrow.cu: memory-bound), the others "wide" (extend_wide.cu: tiles of
+// (extend_narrow.cu: memory-bound), the others "wide" (extend_wide*.cu: tiles of
 // up to 128 rows on the tensor cores).  An item is one (request, key head) of
 // the narrow class or one (row tile, key head) of the wide class; its work is
 // its number of units, blocks of kUnit keys that its last row can see (at
@@ -24,9 +24,12 @@ namespace diffattn {
 constexpr int kUnit = 128;
 constexpr int kNarrowRows = 8;
 constexpr int kWideRows = 128;
-constexpr int kNarrowCost = 0, kWideCost = 3;
+constexpr int kNarrowCost = 0;
+__host__ __device__ constexpr int wide_cost(int d) { return d == 64 ? 2 : 3; }
 constexpr int kNarrowWorkers = 148;  // one CTA per SM
-constexpr int kWideWorkers = 74;     // one CTA pair per two SMs
+// One CTA per SM (both maps), or one CTA pair per two SMs (a map each): two
+// output tiles of 2 d = 128 columns fit tensor memory, two of 256 do not.
+__host__ __device__ constexpr int wide_workers(int d) { return d == 64 ? 148 : 74; }
 
 struct PlanHeader {
   int workers[2];      // workers of the narrow and the wide class
@@ -72,7 +75,7 @@ __host__ __device__ inline PlanLayout plan_layout(const ExtendShape& n) {
   const int tpt = kWideRows / (n.H / n.H_kv);
   l.max_tiles = wide_possible(n) ? n.T / tpt + n.S : 0;
   size_t at = sizeof(PlanHeader);
-  const int workers[2] = {kNarrowWorkers, kWideWorkers};
+  const int workers[2] = {kNarrowWorkers, wide_workers(n.d)};
   for (int c = 0; c < 2; ++c) {
     l.starts[c] = at;
     at += workers[c] * sizeof(WorkStart);
@@ -121,6 +124,6 @@ __device__ inline PlanView plan_view(const void* plan, const ExtendShape& n, int
 }
 
 cudaError_t launch_extend_narrow(const ExtendArgs& a, float* recs, DevCtl ctl, cudaStream_t stream);
-cudaError_t launch_extend_wide(const ExtendArgs& a, float* recs, DevCtl ctl, cudaStream_t stream);
+
 
 }  // namespace diffattn

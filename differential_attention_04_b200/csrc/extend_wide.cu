@@ -1,6 +1,6 @@
 // Attention of requests with more than 8 query rows per key head (chunks of
 // prompts, whole prompts, many heads sharing a key head) over a paged cache,
-// on the tensor cores.
+// on the tensor cores, d = 128.
 //
 // The arithmetic of a tile is that of the dense prefill (prefill_sm100.cu): a
 // cluster of two CTAs takes a tile of up to 128 query rows, CTA rank i
@@ -24,38 +24,26 @@
 //   * The output tile is copied out by warp 3 row by row (a TMA store could not
 //     stop at the end of a request).
 //
-//   * Two warpgroups share the softmax of a tile, 64 keys each of every row:
-//     one alone (the prefill's way) takes longer over a tile than the tensor
-//     cores do.  Their only coupling is the row's maximum, which the two
-//     threads of a row swap through shared memory once a tile.
-//
-// Warp roles (384 threads): warp 0 loads Q_i and K_i, warp 2 loads V, warp 1
+// Warp roles (256 threads): warp 0 loads Q_i and K_i, warp 2 loads V, warp 1
 // owns tensor memory and issues the MMAs, warp 3 copies finished tiles out,
-// warps 4-7 and 8-11 do softmax and epilogue, half a query row per thread.
-// Pipeline and barriers are the prefill's; barrier phases count segments
-// (epi_free), tiles (K, V, S, P) or combined segments (the exchange).
+// warps 4-7 do softmax and epilogue, one query row per thread.  Pipeline and
+// barriers are the prefill's; barrier phases count segments (epi_free), tiles
+// (K, V, S, P) or combined segments (the exchange).
 //
 // Bound: the tensor cores for long chunks (12 d flops per query, key and head);
 // memory for few rows over many keys.
-#include <math.h>
-
-#include "common.cuh"
-#include "extend.cuh"
+#include "extend_wide.cuh"
 
 namespace diffattn {
 
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kSoftmax = 256;  // threads of the two softmax warpgroups
+constexpr int kThreads = 256;
 constexpr int kBM = kWideRows;
 constexpr int kBN = kUnit;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units
-constexpr float kOverflowGuard = 64.0f;    // log2 units
+constexpr int D = 128;
 
-template <int D>
-struct Wide {
+struct C {
   static constexpr int DV = 2 * D;
   static constexpr int HALF = D;                // output columns finished by each CTA
   static constexpr int QBLK = D / 64;           // 128-byte swizzle blocks per Q/K row
@@ -69,8 +57,8 @@ struct Wide {
   static constexpr int OFF_V = OFF_K + 2 * K_BYTES;
   static constexpr int OFF_BAR = OFF_V + 2 * V_BYTES;
   static constexpr int OFF_SSX = OFF_BAR + 256;  // float[128]: the partner's sums of squares
-  static constexpr int OFF_SWAP = OFF_SSX + 512;  // float[2][2][128]: what the two threads of a row swap
-  static constexpr int SMEM = OFF_SWAP + 2048;
+  static constexpr int SMEM_USED = OFF_SSX + 512;
+  static constexpr int SMEM = SMEM_USED + 1024;  // slack for 1024-byte alignment
   static constexpr int EXCH_BYTES = kBM * HALF * 4;
   static constexpr uint32_t TM_S = 0, TM_P = 128, TM_O = 256, TM_COLS = 512;
   static_assert(EXCH_BYTES <= V_BYTES && SMEM <= 232448, "shared memory per CTA");
@@ -90,53 +78,18 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 256, "barriers");
 
-struct WideParams {
-  const void* plan;
-  ExtendShape n;
-  const int* block_table;
-  int max_pages, num_pages, page_shift, max_keys;
-  __nv_bfloat16* o;
-  float* recs;
-  const float* lambda;
-  float lambda_init;
-  const float* rms_w;
-  float eps;
-  int mode;
-  int* status;
-  unsigned long long limit_ns;
-};
+// Wait for every tcgen05.ld issued so far and pin 128 registers behind the wait.
+__device__ __forceinline__ void tmem_ld_wait4(uint32_t (&a)[32], uint32_t (&b)[32], uint32_t (&c)[32],
+                                              uint32_t (&d)[32]) {
+  tmem_ld_wait(a);
+  tmem_ld_wait(b);  // no outstanding loads remain: these only order the registers
+  tmem_ld_wait(c);
+  tmem_ld_wait(d);
+}
 
-// A worker's walk over its segments: units unit .. unit + take - 1 of (row tile at, key head hk).
-struct Walk {
-  WideTile t;
-  int at, hk, unit, take, left;
-  __device__ void open(const WideTile* list) {
-    t = list[at];
-    take = min(left, t.units - unit);
-  }
-  __device__ bool next(const WideTile* list, int H_kv) {  // false: the range is done
-    left -= take;
-    if (left <= 0) return false;
-    unit = 0;
-    if (++at == t.first + t.count) {
-      if (++hk < H_kv) {
-        at = t.first;
-      } else {
-        hk = 0;
-      }
-    }
-    open(list);
-    return true;
-  }
-  __device__ bool begins() const { return unit == 0; }
-  __device__ bool whole() const { return unit == 0 && take == t.units; }
-};
-
-template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     extend_wide_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const WideParams p) {
-  using C = Wide<D>;
   if (!plan_fits(p.plan, p.n, p.status)) return;  // the same for both CTAs of the cluster
   const PlanView pv = plan_view(p.plan, p.n, 1);
   Walk wk;
@@ -152,17 +105,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int causal = pv.head->causal;
   const int H = p.n.H, H_kv = p.n.H_kv, G = H / H_kv, tpt = kBM / G;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = smem_raw;
-  if (smem_u32(smem) & 1023) {  // the swizzled tiles need it; there is no room to align by hand
-    if (threadIdx.x == 0) atomicCAS(p.status, 0, 6);
-    return;
-  }
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem + C::OFF_Q;
   uint8_t* sK = smem + C::OFF_K;
   uint8_t* sV = smem + C::OFF_V;
   Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
   float* ssx = reinterpret_cast<float*>(smem + C::OFF_SSX);
-  float* swap = reinterpret_cast<float*>(smem + C::OFF_SWAP);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();  // 0: map 1, 1: map 2
@@ -176,12 +124,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->k_empty[i], 1);
       mbar_init(&bars->v_full[i], 1);
       mbar_init(&bars->v_empty[i], 1);
-      mbar_init(&bars->p_full[i], kSoftmax / 32);  // one arrival per softmax warp
+      mbar_init(&bars->p_full[i], 4);  // one arrival per softmax warp
       mbar_init(&bars->p_empty[i], 1);
     }
     mbar_init(&bars->v_land, 1);
     mbar_init(&bars->s_full, 1);
-    mbar_init(&bars->s_free, kSoftmax / 32);
+    mbar_init(&bars->s_free, 4);
     mbar_init(&bars->mma_done, 1);
     mbar_init(&bars->exch_full, 1);
     mbar_init(&bars->peer_ready, 1);
@@ -216,20 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int drain_abort = 0;
   const WaitCtl wdrain{p.status, &drain_abort, 1000000000ull};
 
-  // Rows of a page's box, boxes of a full tile, and (in lane b) the first row
-  // of box b of the tile at key0; outside the tensor for a page out of range.
-  const int box_rows = min(1 << p.page_shift, kBN), box_shift = min(p.page_shift, 7);
-  auto boxes_of = [&](int key0, int L) { return L <= key0 ? 0 : (min(kBN, L - key0) + box_rows - 1) >> box_shift; };
-  auto box_row = [&](const WideTile& t, int key0, int boxes) -> int {
-    if (lane >= boxes) return 0;
-    const int key = key0 + (lane << box_shift);
-    const int page = p.block_table[static_cast<size_t>(t.s) * p.max_pages + (key >> p.page_shift)];
-    if (page < 0 || page >= p.num_pages) {
-      atomicCAS(p.status, 0, 6);
-      return -kBN;
-    }
-    return (page << p.page_shift) + (key & ((1 << p.page_shift) - 1));
-  };
+  const TileBoxes box(p);
 
   if (warp == 0) {
     // ---------------------------------------------------- Q / K producer --
@@ -249,14 +184,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int j = 0; j < wk.take; ++j, ++gk) {
         const int st = gk & 1, key0 = (wk.unit + j) * kBN;
-        const int boxes = boxes_of(key0, L), row = box_row(wk.t, key0, boxes);
+        const int boxes = box.count(key0, L), row = box.row(p, wk.t, key0, boxes, lane);
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_empty[st], ((gk >> 1) & 1) ^ 1, wc)))) break;
-        if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[st], boxes * box_rows * 128 * C::QBLK);
+        if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[st], boxes * box.rows * 128 * C::QBLK);
         __syncwarp();
         if (lane < boxes) {
 #pragma unroll
           for (int blk = 0; blk < C::QBLK; ++blk)
-            tma_load_4d(sK + st * C::K_BYTES + blk * C::BLK_BYTES + lane * box_rows * 128, &tk, &bars->k_full[st],
+            tma_load_4d(sK + st * C::K_BYTES + blk * C::BLK_BYTES + lane * box.rows * 128, &tk, &bars->k_full[st],
                         blk * 64, 2 * wk.hk + static_cast<int>(rank), row, 0);
         }
       }
@@ -275,27 +210,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (k > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&bars->epi_free, (k - 1) & 1, wc)))) break;
       for (int j = 0; j < wk.take; ++j, ++gv) {
         const int st = gv & 1, key0 = (wk.unit + j) * kBN;
-        const int boxes = boxes_of(key0, L), row = box_row(wk.t, key0, boxes);
+        const int boxes = box.count(key0, L), row = box.row(p, wk.t, key0, boxes, lane);
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_empty[st], ((gv >> 1) & 1) ^ 1, wc)))) break;
         const bool full = key0 + kBN <= L;
         uint64_t* bar = full ? &bars->v_full[st] : &bars->v_land;
         uint8_t* dst = sV + st * C::V_BYTES;
-        if (lane == 0) mbar_arrive_expect_tx(bar, boxes * box_rows * 128 * C::VBLK);
+        if (lane == 0) mbar_arrive_expect_tx(bar, boxes * box.rows * 128 * C::VBLK);
         __syncwarp();
         if (lane < boxes) {
 #pragma unroll
           for (int blk = 0; blk < C::VBLK; ++blk)
-            tma_load_4d(dst + blk * C::BLK_BYTES + lane * box_rows * 128, &tv, bar, blk * 64, wk.hk, row, 0);
+            tma_load_4d(dst + blk * C::BLK_BYTES + lane * box.rows * 128, &tv, bar, blk * 64, wk.hk, row, 0);
         }
         if (!full) {
           mbar_wait(&bars->v_land, ragged & 1, wdrain);
           ++ragged;
-          const int live = max(0, L - key0), chunks = (kBN - live) * 8;  // 16-byte chunks to clear in a block
-          for (int i = lane; i < chunks * C::VBLK; i += 32)
-            *reinterpret_cast<uint4*>(dst + (i / chunks) * C::BLK_BYTES + live * 128 + (i % chunks) * 16) =
-                make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();  // the product reads them through the async proxy
-          __syncwarp();
+          clear_v_rows(dst, C::VBLK, max(0, L - key0), lane);
           if (lane == 0) mbar_arrive(&bars->v_full[st]);
         }
       }
@@ -367,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int own0 = (rank == 0) ? 0 : C::HALF;
     do {
       if (!wk.whole()) continue;
-      named_bar_sync(2, kSoftmax + 32);  // with the softmax warps' arrivals
+      named_bar_sync(2, 160);  // with the softmax warps' arrivals
       const int rows = wk.t.ntok * G, chunk = lane & 7;
 #pragma unroll
       for (int blk = 0; blk < C::HALF / 64; ++blk) {
@@ -390,29 +320,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 4) {
     // ------------------------------------------------ softmax + epilogue --
-    const int quarter = warp & 3, wg = (warp >> 2) - 1;
+    const int quarter = warp & 3;
     const int r = quarter * 32 + lane;  // query row within the tile (= TMEM lane)
     const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const float coef2 = map2_coefficient(p.mode, *p.lambda);  // c in softmax(S1) + c softmax(S2)
     const float sc = kLog2e * rsqrtf(static_cast<float>(D));
     constexpr int HALF = C::HALF;
-    constexpr int MINE = HALF / 2;  // columns of each half of O that this thread sends or finishes
-    constexpr int NC = MINE / 4;    // float4 chunks per exchanged row
-    constexpr int KEYS = kBN / 2;
-    // V stage 0 receives the partner's half, stage 1 holds the half sent, then the output; this warpgroup's part
-    float* recv = reinterpret_cast<float*>(sV) + wg * kBM * MINE;
-    float* stage = reinterpret_cast<float*>(sV + C::V_BYTES) + wg * kBM * MINE;
+    constexpr int NC = HALF / 4;  // float4 chunks per exchanged row
+    float* recv = reinterpret_cast<float*>(sV);                // V stage 0: the partner's half
+    float* stage = reinterpret_cast<float*>(sV + C::V_BYTES);  // V stage 1: the half sent, then the output
     const uint32_t own0 = (rank == 0) ? 0 : HALF;   // columns this CTA finishes
     const uint32_t send0 = (rank == 0) ? HALF : 0;  // columns it hands to the partner
-    // The two threads of a row hand each other a value (both warps of the pair always take part, also
-    // after an abort).  Two buffers: a value is read before the next but one is written.
-    int swaps = 0;
-    auto swap_value = [&](float v) -> float {
-      float* at = swap + (swaps++ & 1) * 2 * kBM;
-      at[wg * kBM + r] = v;
-      named_bar_sync(3 + quarter, 64);
-      return at[(wg ^ 1) * kBM + r];
-    };
     int g = 0;   // S / P tiles consumed
     int ke = 0;  // segments combined
     bool sm_ok = true;
@@ -420,74 +338,66 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int L = min(wk.t.L, p.max_keys);
       const int lim = min(wk.t.lim0 + (causal ? r / G : 0), L - 1);  // last key that this row sees
       const bool live = r < wk.t.ntok * G;
-      float m_run = -INFINITY, l_run = 0.f;  // l_run: of this thread's keys
-      // this thread's half of O, and l, *= alpha (the whole warp takes part; alpha = 1 leaves a row as it is)
+      float m_run = -INFINITY, l_run = 0.f;
+      // O and l *= alpha (the whole warp takes part; alpha = 1 leaves a row as it is)
       auto rescale_o = [&](float alpha) {
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < C::DV / 32; ++c) {
           uint32_t ov[32];
-          tmem_ld32_sync(tl + C::TM_O + wg * D + 32 * c, ov);
+          tmem_ld32_sync(tl + C::TM_O + 32 * c, ov);
 #pragma unroll
           for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-          tmem_st32(tl + C::TM_O + wg * D + 32 * c, ov);
+          tmem_st32(tl + C::TM_O + 32 * c, ov);
         }
         tmem_st_wait();
         l_run *= alpha;
       };
-      for (int j = 0; j < wk.take; ++j, ++g) {
+      const int g_end = g + wk.take;
+      for (int j = 0; sm_ok && j < wk.take; ++j, ++g) {
         const int bb = g & 1;
         // every exit is taken by the whole warp (a wait may end differently in its lanes)
-        if (sm_ok) sm_ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full, g & 1, wc));
-        if (!sm_ok) {  // the other warp of the pair may not have seen the abort yet
-          if (j == 0) swap_value(0.f);
-          swap_value(0.f);
-          continue;
-        }
+        if (!(sm_ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full, g & 1, wc)))) break;
         // S_g has completed, and with it every MMA issued before it, PV_{g-2}
         // included: P buffer b is free.
         tc_fence_after();
-        uint32_t s0[32], s1[32];
-        tmem_ld32(tl + C::TM_S + wg * KEYS, s0);
-        tmem_ld32(tl + C::TM_S + wg * KEYS + 32, s1);
-        tmem_ld_wait(s0);
-        tmem_ld_wait(s1);
+        uint32_t s0[32], s1[32], s2[32], s3[32];
+        tmem_ld32(tl + C::TM_S + 0, s0);
+        tmem_ld32(tl + C::TM_S + 32, s1);
+        tmem_ld32(tl + C::TM_S + 64, s2);
+        tmem_ld32(tl + C::TM_S + 96, s3);
+        tmem_ld_wait4(s0, s1, s2, s3);
         // S is in registers: the next S tile may overwrite the buffer
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->s_free);
-        float x[KEYS];
+        float x[128];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           x[i] = __uint_as_float(s0[i]);
           x[32 + i] = __uint_as_float(s1[i]);
+          x[64 + i] = __uint_as_float(s2[i]);
+          x[96 + i] = __uint_as_float(s3[i]);
         }
-        const int last = lim - (wk.unit + j) * kBN - wg * KEYS;  // last visible one of these keys
-        if (last < KEYS - 1) {
+        const int last = lim - (wk.unit + j) * kBN;  // last visible key of the tile
+        if (last < kBN - 1) {
 #pragma unroll
-          for (int i = 0; i < KEYS; ++i)
+          for (int i = 0; i < 128; ++i)
             if (i > last) x[i] = -INFINITY;
         }
-        auto max8 = [](const float (&mk)[8]) {
-          return fmaxf(fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])), fmaxf(fmaxf(mk[4], mk[5]), fmaxf(mk[6], mk[7])));
-        };
         if (j == 0) {  // the first tile sets the reference maximum
           float mk[8];
 #pragma unroll
           for (int c = 0; c < 8; ++c) mk[c] = x[c];
 #pragma unroll
-          for (int i = 8; i < KEYS; i += 8) {
+          for (int i = 8; i < 128; i += 8) {
 #pragma unroll
             for (int c = 0; c < 8; ++c) mk[c] = fmaxf(mk[c], x[i + c]);
           }
-          const float mine = max8(mk) * sc;
-          m_run = fmaxf(mine, swap_value(mine));
+          m_run = fmaxf(fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])), fmaxf(fmaxf(mk[4], mk[5]), fmaxf(mk[6], mk[7]))) * sc;
         }
         // P = exp2(s*c - m_run) into P[b], taken relative to the reference
         // maximum m_run as it stands; the tile's own maximum is formed
         // alongside.  A row without keys keeps the maximum -inf: all its P are 0.
-        // P is rounded to bf16, as in the dense prefill: the remainders would be
-        // a second product (see extend_narrow.cu, where it is free; here the
-        // products bound the time).
         float lsum = 0.f, t_mx = -INFINITY;
         auto make_p = [&](bool with_max) {
           const float mneg = m_run == -INFINITY ? 0.f : -m_run;
@@ -495,30 +405,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           float mk[8];
 #pragma unroll
           for (int c = 0; c < 8; ++c) mk[c] = -INFINITY;
-          uint32_t pk[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float a0 = x[2 * i], a1 = x[2 * i + 1];
-            if (with_max) mk[i & 7] = fmaxf(mk[i & 7], fmaxf(a0, a1));
-            const float p0 = fast_exp2(fmaf(a0, sc, mneg));
-            const float p1 = fast_exp2(fmaf(a1, sc, mneg));
-            acc[i & 3] += p0 + p1;
-            pk[i] = pack_bf16x2(p0, p1);
+          for (int half = 0; half < 2; ++half) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float a0 = x[64 * half + 2 * i], a1 = x[64 * half + 2 * i + 1];
+              if (with_max) mk[i & 7] = fmaxf(mk[i & 7], fmaxf(a0, a1));
+              const float p0 = fast_exp2(fmaf(a0, sc, mneg));
+              const float p1 = fast_exp2(fmaf(a1, sc, mneg));
+              acc[i & 3] += p0 + p1;
+              pk[i] = pack_bf16x2(p0, p1);
+            }
+            tmem_st32(tl + C::TM_P + 64 * bb + 32 * half, pk);
           }
-          tmem_st32(tl + C::TM_P + 64 * bb + 32 * wg, pk);
           lsum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-          if (with_max) t_mx = max8(mk) * sc;
+          if (with_max)
+            t_mx = fmaxf(fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])), fmaxf(fmaxf(mk[4], mk[5]), fmaxf(mk[6], mk[7]))) * sc;
         };
         make_p(true);
-        t_mx = fmaxf(t_mx, swap_value(t_mx));
         // A jump of the maximum by more than 2^64 would overflow P: rescale O
-        // to the new maximum (after the previous tile's PV has completed) and
-        // redo P.  Both threads of a row decide alike.
+        // to the new maximum (after the previous tile's PV has completed) and redo P.
         const bool hard = j > 0 && t_mx > m_run + kOverflowGuard;
         if (__any_sync(0xffffffffu, hard)) {
           tmem_st_wait();
-          sm_ok = __all_sync(0xffffffffu, mbar_wait(&bars->p_empty[(g - 1) & 1], ((g - 1) >> 1) & 1, wc));
-          if (!sm_ok) continue;
+          if (!(sm_ok = __all_sync(0xffffffffu, mbar_wait(&bars->p_empty[(g - 1) & 1], ((g - 1) >> 1) & 1, wc))))
+            break;
           tc_fence_after();
           rescale_o(hard ? fast_exp2(m_run - t_mx) : 1.0f);
           if (hard) m_run = t_mx;
@@ -533,27 +445,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         // O is rescaled once this tile's PV (which used the old reference) has completed.
         const bool need = t_mx > m_run + kRescaleThreshold;
         if (__any_sync(0xffffffffu, need)) {
-          sm_ok = __all_sync(0xffffffffu, mbar_wait(&bars->p_empty[bb], (g >> 1) & 1, wc));
-          if (!sm_ok) continue;
+          if (!(sm_ok = __all_sync(0xffffffffu, mbar_wait(&bars->p_empty[bb], (g >> 1) & 1, wc)))) break;
           tc_fence_after();
           rescale_o(need ? fast_exp2(m_run - t_mx) : 1.0f);
           if (need) m_run = t_mx;
         }
       }
+      g = g_end;  // the loop may stop early after an abort: keep the tile count in step
 
       // ------------------------------------------------------ epilogue --
       // O is complete once the segment's last PV (and with it every earlier MMA) has.
-      l_run += swap_value(l_run);
       if (sm_ok) sm_ok = mbar_wait(&bars->p_empty[(g - 1) & 1], ((g - 1) >> 1) & 1, wc);
       tc_fence_after();
       if (!wk.whole()) {
         // a part of the row's keys: this map's sums to the worker's record
         float* rec = p.recs + (2 * (blockIdx.x >> 1) + (wk.begins() ? 1 : 0)) * record_floats(kBM, D);
-        float* orow = rec + 4 * kBM + static_cast<size_t>(r) * 2 * C::DV + rank * C::DV + wg * D;
+        float* orow = rec + 4 * kBM + static_cast<size_t>(r) * 2 * C::DV + rank * C::DV;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < C::DV / 32; ++c) {
           uint32_t ov[32];
-          tmem_ld32_sync(tl + C::TM_O + wg * D + 32 * c, ov);
+          tmem_ld32_sync(tl + C::TM_O + 32 * c, ov);
           if (live) {
 #pragma unroll
             for (int f = 0; f < 8; ++f)
@@ -561,27 +472,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                   make_uint4(ov[4 * f + 0], ov[4 * f + 1], ov[4 * f + 2], ov[4 * f + 3]);
           }
         }
-        if (live && wg == 0) *reinterpret_cast<float2*>(rec + 4 * r + 2 * rank) = make_float2(m_run, l_run);
+        if (live) *reinterpret_cast<float2*>(rec + 4 * r + 2 * rank) = make_float2(m_run, l_run);
         tc_fence_before();
-        named_bar_sync(1, kSoftmax);  // every row's tensor-memory reads are done
+        named_bar_sync(1, 128);  // every row's tensor-memory reads are done
         if (tid == 128) mbar_arrive(&bars->epi_free);  // the next segment's first PV may overwrite O
         __syncwarp();
         continue;
       }
       // Both V stages are free of this segment's PV products: announce that
       // this CTA's receive buffer is ready, with the exchange barrier armed first.
-      named_bar_sync(1, kSoftmax);
+      named_bar_sync(1, 128);
       if (tid == 128) {
         mbar_arrive_expect_tx(&bars->exch_full, C::EXCH_BYTES);
         mbar_arrive_expect_tx(&bars->ss_full, kBM * 4);  // the partner's sums of squares, by st.async
         mbar_arrive_remote(map_to_cta(smem_u32(&bars->peer_ready), partner));
       }
       const float inv = l_run > 0.f ? ((rank == 0) ? 1.0f / l_run : coef2 / l_run) : 0.f;
-      float* srow = stage + r * MINE;
+      float* srow = stage + r * HALF;
 #pragma unroll
-      for (int c = 0; c < MINE / 32; ++c) {
+      for (int c = 0; c < HALF / 32; ++c) {
         uint32_t ov[32];
-        tmem_ld32_sync(tl + C::TM_O + send0 + wg * MINE + 32 * c, ov);
+        tmem_ld32_sync(tl + C::TM_O + send0 + 32 * c, ov);
 #pragma unroll
         for (int f = 0; f < 8; ++f) {
           const int chunk = (c * 8 + f) ^ (r % NC);
@@ -595,19 +506,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the partner's receive buffer must be free before this CTA writes into it
       const bool peer_ok = mbar_wait_acq_cluster(&bars->peer_ready, ke & 1, wc);
       if (lane == 0 && peer_ok) {
-        const int off = quarter * 32 * MINE;  // this warp's 32 rows, contiguous
-        bulk_copy_s2cluster(map_to_cta(smem_u32(recv + off), partner), stage + off, 32 * MINE * 4,
+        const int off = quarter * 32 * HALF;  // this warp's 32 rows, contiguous
+        bulk_copy_s2cluster(map_to_cta(smem_u32(recv + off), partner), stage + off, 32 * HALF * 4,
                             map_to_cta(smem_u32(&bars->exch_full), partner));
         bulk_commit_group();
       }
       mbar_wait(&bars->exch_full, ke & 1, wdrain);  // the partner's half has landed (even after an abort)
-      float y[MINE];
+      float y[HALF];
       float ss = 0.f;
-      const float* rrow = recv + r * MINE;
+      const float* rrow = recv + r * HALF;
 #pragma unroll
-      for (int c = 0; c < MINE / 32; ++c) {
+      for (int c = 0; c < HALF / 32; ++c) {
         uint32_t ov[32];
-        tmem_ld32_sync(tl + C::TM_O + own0 + wg * MINE + 32 * c, ov);
+        tmem_ld32_sync(tl + C::TM_O + own0 + 32 * c, ov);
 #pragma unroll
         for (int f = 0; f < 8; ++f) {
           const int chunk = (c * 8 + f) ^ (r % NC);
@@ -621,28 +532,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // the row's sum of squares over this CTA's columns, to the partner: an
-      // asynchronous store that completes on the partner's barrier (armed
-      // before its receive buffer was announced)
-      ss += swap_value(ss);
-      if (peer_ok && wg == 0)
+      // this row's half of the sum of squares to the partner: an asynchronous
+      // store that completes on the partner's barrier (armed before its
+      // receive buffer was announced)
+      if (peer_ok)
         st_async_f32(map_to_cta(smem_u32(ssx + r), partner), ss, map_to_cta(smem_u32(&bars->ss_full), partner));
       if (lane == 0 && peer_ok) bulk_wait_group_read0();  // the outgoing copy has left the staging rows
       __syncwarp();
-      named_bar_sync(1, kSoftmax);  // every warp's outgoing copy is done with the rows the output tile reuses
+      named_bar_sync(1, 128);  // every warp's outgoing copy is done with the rows the output tile reuses
       mbar_wait_acq_cluster(&bars->ss_full, ke & 1, wdrain);
       const float rs = rsqrtf((ss + ssx[r]) / static_cast<float>(C::DV) + p.eps);
       const float gsc = (1.0f - p.lambda_init) * rs;
       // bf16 tile [64-column block][128 rows][64 columns], 128-byte swizzle, in the staging stage
-      const uint32_t sout = smem_u32(sV + C::V_BYTES);
+      const uint32_t sout = smem_u32(stage);
 #pragma unroll
-      for (int i = 0; i < MINE / 8; ++i) {
-        const int c8 = wg * (MINE / 8) + i;  // 16-byte chunk of the output row
+      for (int c8 = 0; c8 < HALF / 8; ++c8) {
         uint32_t w4[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int c = own0 + 8 * c8 + 2 * e;
-          w4[e] = pack_bf16x2(y[8 * i + 2 * e] * gsc * __ldg(p.rms_w + c), y[8 * i + 2 * e + 1] * gsc * __ldg(p.rms_w + c + 1));
+          const int c = 8 * c8 + 2 * e;
+          w4[e] = pack_bf16x2(y[c] * gsc * __ldg(p.rms_w + own0 + c), y[c + 1] * gsc * __ldg(p.rms_w + own0 + c + 1));
         }
         const uint32_t a = sout + (c8 / 8) * C::BLK_BYTES + r * 128 + (((c8 % 8) ^ (r & 7)) << 4);
         st_shared_v4(a, w4[0], w4[1], w4[2], w4[3]);
@@ -650,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++ke;
       // hand the staged tile to warp 3, which copies it out and frees the V
       // stages, and go on with the next segment
-      named_bar_arrive(2, kSoftmax + 32);
+      named_bar_arrive(2, 160);
     } while (wk.next(pv.wide, H_kv));
   }
 
@@ -663,21 +572,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
-cudaError_t launch_d(const ExtendArgs& a, float* recs, DevCtl ctl, cudaStream_t stream) {
-  using C = Wide<D>;
-  static unsigned long long set_ctx[64] = {};
-  if (ctl.dev < 0 || ctl.dev >= 64) return cudaErrorInvalidDevice;
-  if (ctl.ctx == 0 || set_ctx[ctl.dev] != ctl.ctx) {
-    const auto fn = extend_wide_kernel<D>;
-    cudaError_t e;
-    if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(fn, cudaFuncAttributeRequiredClusterWidth, 2)) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(fn, cudaFuncAttributeRequiredClusterHeight, 1)) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(fn, cudaFuncAttributeRequiredClusterDepth, 1)) != cudaSuccess)
-      return e;
-    set_ctx[ctl.dev] = ctl.ctx;
-  }
+}  // namespace
+
+WideParams wide_params(const ExtendArgs& a, float* recs, DevCtl ctl) {
   WideParams p = {};
   p.plan = a.plan;
   p.n = a.n;
@@ -696,17 +593,28 @@ cudaError_t launch_d(const ExtendArgs& a, float* recs, DevCtl ctl, cudaStream_t 
   p.mode = a.mode;
   p.status = ctl.status;
   p.limit_ns = ctl.limit_ns;
+  return p;
+}
+
+cudaError_t launch_extend_wide128(const ExtendArgs& a, float* recs, DevCtl ctl, cudaStream_t stream) {
+  static unsigned long long set_ctx[64] = {};
+  if (ctl.dev < 0 || ctl.dev >= 64) return cudaErrorInvalidDevice;
+  if (ctl.ctx == 0 || set_ctx[ctl.dev] != ctl.ctx) {
+    const auto fn = extend_wide_kernel;
+    cudaError_t e;
+    if ((e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(fn, cudaFuncAttributeRequiredClusterWidth, 2)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(fn, cudaFuncAttributeRequiredClusterHeight, 1)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(fn, cudaFuncAttributeRequiredClusterDepth, 1)) != cudaSuccess)
+      return e;
+    set_ctx[ctl.dev] = ctl.ctx;
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * kWideWorkers, 1, 1);
+  cfg.gridDim = dim3(2 * wide_workers(D), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, extend_wide_kernel<D>, a.tq, a.tk, a.tv, p);
-}
-}  // namespace
-
-cudaError_t launch_extend_wide(const ExtendArgs& a, float* recs, DevCtl ctl, cudaStream_t stream) {
-  return a.n.d == 128 ? launch_d<128>(a, recs, ctl, stream) : launch_d<64>(a, recs, ctl, stream);
+  return cudaLaunchKernelEx(&cfg, extend_wide_kernel, a.tq, a.tk, a.tv, wide_params(a, recs, ctl));
 }
 
 }  // namespace diffattn
