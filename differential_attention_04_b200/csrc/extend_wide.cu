@@ -78,15 +78,6 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 256, "barriers");
 
-// Wait for every tcgen05.ld issued so far and pin 128 registers behind the wait.
-__device__ __forceinline__ void tmem_ld_wait4(uint32_t (&a)[32], uint32_t (&b)[32], uint32_t (&c)[32],
-                                              uint32_t (&d)[32]) {
-  tmem_ld_wait(a);
-  tmem_ld_wait(b);  // no outstanding loads remain: these only order the registers
-  tmem_ld_wait(c);
-  tmem_ld_wait(d);
-}
-
 __global__ void __launch_bounds__(kThreads, 1)
     extend_wide_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const WideParams p) {
@@ -360,24 +351,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // S_g has completed, and with it every MMA issued before it, PV_{g-2}
         // included: P buffer b is free.
         tc_fence_after();
-        uint32_t s0[32], s1[32], s2[32], s3[32];
-        tmem_ld32(tl + C::TM_S + 0, s0);
-        tmem_ld32(tl + C::TM_S + 32, s1);
-        tmem_ld32(tl + C::TM_S + 64, s2);
-        tmem_ld32(tl + C::TM_S + 96, s3);
-        tmem_ld_wait4(s0, s1, s2, s3);
+        uint32_t su[128];
+        tmem_ld128_sync(tl + C::TM_S, su);
         // S is in registers: the next S tile may overwrite the buffer
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->s_free);
         float x[128];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          x[i] = __uint_as_float(s0[i]);
-          x[32 + i] = __uint_as_float(s1[i]);
-          x[64 + i] = __uint_as_float(s2[i]);
-          x[96 + i] = __uint_as_float(s3[i]);
-        }
+        for (int i = 0; i < 128; ++i) x[i] = __uint_as_float(su[i]);
         const int last = lim - (wk.unit + j) * kBN;  // last visible key of the tile
         if (last < kBN - 1) {
 #pragma unroll

@@ -10,21 +10,24 @@
 // (As a cluster of two CTAs with a map each, extend_wide.cu's way, ragged
 // prompts of 8 K tokens over 16 heads took 335 us, WIDE64_US this way.)
 //
-// Tensor memory: S_m (128 columns) at 128 m, O_m (128 columns) at 256 + 128 m.
-// P_m (bf16, 64 columns) takes the first half of S_m's columns: a thread owns
-// its row's lane, so it may overwrite scores that it has read.  It takes the
-// row in two halves of 64 keys, which keeps it within 168 registers; the P of
-// a half only covers scores that are in registers by then.
+// Tensor memory: the scores of map m are taken 64 keys at a time into two
+// buffers, at 128 m and 128 m + 64; O_m (128 columns) is at 256 + 128 m.  P_m
+// (bf16, 32 columns) takes the first half of its scores' columns: a thread
+// owns its row's lane, so it may overwrite scores that it has read.  With one
+// buffer of 128 keys a map's scores, softmax and product ran one after the
+// other and a tile of 128 keys took 4300 cycles.
 //
-// Order of the products (one thread, an in-order pipe):
-//   S_A(0) S_B(0) | PV_A(j) S_A(j+1) PV_B(j) S_B(j+1) | ...
-// PV_m(j) waits for p_full[m], which also says that S_m(j) has been read, so
-// S_m(j+1) needs no barrier of its own; it overwrites P_m(j) behind the product
-// that reads it.
+// Order of a map's products (one thread, an in-order pipe), t counting 64 keys:
+//   S(0) | S(t+1) PV(t) | ...
+// PV(t) waits for p_full, which also says that S(t) has been read, so S(t+2)
+// needs no barrier of its own; it overwrites P(t) behind the product that
+// reads it.  Each map has an issuing thread: commits and waits take as long as
+// the products, and one thread's fall under the other's products (one thread
+// for both maps: ONE_ISSUER).
 //
 // Warp roles (384 threads): warp 0 loads Q and K (both maps), warp 2 loads V,
-// warp 1 owns tensor memory and issues the MMAs, warps 4-7 and 8-11 are the
-// maps' softmax and epilogue, one query row per thread.  In the epilogue the
+// warps 1 and 3 issue a map's MMAs each (warp 1 owns tensor memory), warps 4-7
+// and 8-11 are the maps' softmax and epilogue, one query row per thread.  In the epilogue the
 // two threads of a row swap halves of their normalised sums through shared
 // memory (a barrier between the two warps of a row quarter, none over the
 // CTA), so each finishes 64 of the 128 channels.
@@ -41,6 +44,7 @@ constexpr int D = 64;
 constexpr int kThreads = 384;
 constexpr int kBM = kWideRows;
 constexpr int kBN = kUnit;
+constexpr int kHalf = kBN / 2;  // keys of a step of the softmax
 
 struct C {
   static constexpr int DV = 2 * D;
@@ -64,10 +68,12 @@ struct Bars {
   uint64_t k_full[2], k_empty[2];
   uint64_t v_full[2], v_empty[2];
   uint64_t v_land;      // a ragged V tile has landed; the rows behind the last key are still to be zeroed
-  uint64_t s_full[2];   // per map: a tile's scores are there
-  uint64_t p_full[2];   // per map: its weights are there (and its scores have been read)
-  uint64_t pv_done[2];  // per map: its product is done
-  uint64_t o_free[2];   // per map and segment: O has been read
+  uint64_t s_full[2][2];  // per map and buffer: 64 keys' scores are there
+  uint64_t p_full[2][2];  // their weights are there (and the scores have been read)
+  // their product is done (a barrier per buffer: with one per map, a wait could
+  // take the phase before the last for the one that it means)
+  uint64_t pv_done[2][2];
+  uint64_t o_free[2];     // per map and segment: O has been read
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort;
@@ -105,19 +111,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     mbar_init(&bars->q_full, 1);
-    mbar_init(&bars->q_empty, 1);
+    mbar_init(&bars->q_empty, 2);  // both maps' products have read it, as for K and V
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->k_full[i], 1);
-      mbar_init(&bars->k_empty[i], 1);
+      mbar_init(&bars->k_empty[i], 2);
       mbar_init(&bars->v_full[i], 1);
-      mbar_init(&bars->v_empty[i], 1);
-      mbar_init(&bars->s_full[i], 1);
-      mbar_init(&bars->p_full[i], 4);  // one arrival per softmax warp
-      mbar_init(&bars->pv_done[i], 1);
+      mbar_init(&bars->v_empty[i], 2);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&bars->s_full[i][b], 1);
+        mbar_init(&bars->p_full[i][b], 4);  // one arrival per softmax warp
+        mbar_init(&bars->pv_done[i][b], 1);
+      }
       mbar_init(&bars->o_free[i], 4);
     }
     mbar_init(&bars->v_land, 1);
-    mbar_init(&bars->mma_done, 1);
+    mbar_init(&bars->mma_done, 2);
     bars->abort = 0;
     fence_mbarrier_init();
   }
@@ -211,51 +219,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int j = max(0, gv - 2); j < gv; ++j) mbar_wait(&bars->v_full[j & 1], (j >> 1) & 1, wdrain);
     __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------- MMA issuer --
+  } else if (warp == 1 || warp == 3) {
+    // ------------------------------------- MMA issuers, one for each map --
     if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
+      constexpr uint32_t idesc_s = idesc_bf16_f32(128, kHalf, false, false);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(128, C::DV, false, true);
-      const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK), sVa = smem_u32(sV);
-      int gs = 0;  // tiles whose S products have been issued
+      const int m = warp >> 1;
+      const uint32_t sQa = smem_u32(sQ) + m * C::MAP_BYTES, sKa = smem_u32(sK) + m * C::MAP_BYTES, sVa = smem_u32(sV);
+      const uint32_t t_s = tmem + C::TM_S + 128 * m, t_o = tmem + C::TM_O + 128 * m;
+      int gs = 0;  // halves of tiles whose S products have been issued
       int gp = 0;  // and whose PV products have
-      // S of map m for tile gs; map 0 comes first, map 1 completes the tile
-      auto issue_s = [&](int m, bool last) -> bool {
-        const int st = gs & 1;
-        if (m == 0 && !mbar_wait(&bars->k_full[st], (gs >> 1) & 1, wc)) return false;
+      // S for half gs & 1 of tile gs / 2
+      auto issue_s = [&](bool last) -> bool {
+        const int st = (gs >> 1) & 1, b = gs & 1;
+        if (b == 0 && !mbar_wait(&bars->k_full[st], (gs >> 2) & 1, wc)) return false;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)  // each instruction takes 32 bytes of every row
-          umma_ss(tmem + C::TM_S + 128 * m, smem_desc_sw128(sQa + m * C::MAP_BYTES + kk * 32, 16, 1024),
-                  smem_desc_sw128(sKa + (2 * st + m) * C::MAP_BYTES + kk * 32, 16, 1024), idesc_s, kk > 0 ? 1u : 0u);
-        umma_commit(&bars->s_full[m]);
-        if (m == 1) {
-          umma_commit(&bars->k_empty[st]);
-          if (last) umma_commit(&bars->q_empty);
-          ++gs;
-        }
+          umma_ss(t_s + kHalf * b, smem_desc_sw128(sQa + kk * 32, 16, 1024),
+                  smem_desc_sw128(sKa + 2 * st * C::MAP_BYTES + b * kHalf * 128 + kk * 32, 16, 1024), idesc_s,
+                  kk > 0 ? 1u : 0u);
+        umma_commit(&bars->s_full[m][b]);
+        if (b == 1) umma_commit(&bars->k_empty[st]);
+        if (last) umma_commit(&bars->q_empty);
+        ++gs;
         return true;
       };
       bool ok = true;
       for (int k = 0; ok; ++k) {
-        ok = mbar_wait(&bars->q_full, k & 1, wc) && issue_s(0, false) && issue_s(1, wk.take == 1);
-        for (int j = 0; ok && j < wk.take; ++j, ++gp) {
-          const int st = gp & 1;
-          for (int m = 0; ok && m < 2; ++m) {
-            if (!(ok = mbar_wait(&bars->p_full[m], gp & 1, wc))) break;
-            if (m == 0 && !(ok = mbar_wait(&bars->v_full[st], (gp >> 1) & 1, wc))) break;
-            // a new segment's O replaces the last one's once that has been read
-            if (j == 0 && k > 0 && !(ok = mbar_wait(&bars->o_free[m], (k - 1) & 1, wc))) break;
-            tc_fence_after();
+        const int n = 2 * wk.take;
+        ok = mbar_wait(&bars->q_full, k & 1, wc) && issue_s(false);
+        for (int t = 0; ok && t < n; ++t, ++gp) {
+          if (t + 1 < n && !(ok = issue_s(t + 2 == n))) break;
+          const int st = (gp >> 1) & 1, b = gp & 1;
+          if (!(ok = mbar_wait(&bars->p_full[m][b], (gp >> 1) & 1, wc))) break;
+          if (b == 0 && !(ok = mbar_wait(&bars->v_full[st], (gp >> 2) & 1, wc))) break;
+          // a new segment's O replaces the last one's once that has been read
+          if (t == 0 && k > 0 && !(ok = mbar_wait(&bars->o_free[m], (k - 1) & 1, wc))) break;
+          tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < kBN / 16; ++kk)
-              umma_ts(tmem + C::TM_O + 128 * m, tmem + C::TM_S + 128 * m + 8 * kk,
-                      smem_desc_sw128(sVa + st * C::V_BYTES + kk * 2048, C::BLK_BYTES, 1024), idesc_pv,
-                      (j > 0 || kk > 0) ? 1u : 0u);
-            umma_commit(&bars->pv_done[m]);
-            if (m == 1) umma_commit(&bars->v_empty[st]);
-            if (j + 1 < wk.take) ok = issue_s(m, j + 2 == wk.take);
-          }
+          for (int kk = 0; kk < kHalf / 16; ++kk)
+            umma_ts(t_o, t_s + kHalf * b + 8 * kk,
+                    smem_desc_sw128(sVa + st * C::V_BYTES + (b * (kHalf / 16) + kk) * 2048, C::BLK_BYTES, 1024),
+                    idesc_pv, (t > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&bars->pv_done[m][b]);
+          if (b == 1) umma_commit(&bars->v_empty[st]);
         }
         if (!ok || !wk.next(pv.wide, H_kv)) break;
       }
@@ -276,14 +284,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sc = kLog2e * rsqrtf(static_cast<float>(D));
     float* swap = reinterpret_cast<float*>(smem + C::OFF_SWAP);
     float* ssx = reinterpret_cast<float*>(smem + C::OFF_SS);
-    int g = 0;  // tiles consumed
+    int g = 0;  // halves of tiles consumed
     bool sm_ok = true;
     do {
       const int L = min(wk.t.L, p.max_keys);
       const int lim = min(wk.t.lim0 + (causal ? r / G : 0), L - 1);  // last key that this row sees
       const bool live = r < wk.t.ntok * G;
       float m_run = -INFINITY, l_run = 0.f;
-      const int g_end = g + wk.take;
+      const int n = 2 * wk.take, g_end = g + n;
       // O *= alpha (the whole warp takes part; alpha = 1 leaves a row as it is)
       auto rescale_o = [&](float alpha) {
 #pragma unroll
@@ -297,108 +305,84 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         l_run *= alpha;
       };
-      for (int j = 0; sm_ok && j < wk.take; ++j, ++g) {
+      for (int t = 0; sm_ok && t < n; ++t, ++g) {
+        const int b = g & 1;
         // every exit is taken by the whole warp (a wait may end differently in its lanes)
-        if (!(sm_ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[map], g & 1, wc)))) break;
+        if (!(sm_ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[map][b], (g >> 1) & 1, wc)))) break;
         tc_fence_after();
-        const int last = lim - (wk.unit + j) * kBN;  // last visible key of the tile
-        float t_mx = -INFINITY;
+        uint32_t su[kHalf];
+        tmem_ld64_sync(t_s + kHalf * b, su);
+        float x[kHalf];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t s0[32], s1[32];
-          tmem_ld32(t_s + 64 * half, s0);
-          tmem_ld32(t_s + 64 * half + 32, s1);
-          tmem_ld_wait(s0);
-          tmem_ld_wait(s1);
-          float x[64];
+        for (int i = 0; i < kHalf; ++i) x[i] = __uint_as_float(su[i]);
+        const int last = lim - wk.unit * kBN - t * kHalf;  // last visible one of these keys
+        if (last < kHalf - 1) {
+#pragma unroll
+          for (int i = 0; i < kHalf; ++i)
+            if (i > last) x[i] = -INFINITY;
+        }
+        auto max8 = [](const float (&mk)[8]) {
+          return fmaxf(fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])), fmaxf(fmaxf(mk[4], mk[5]), fmaxf(mk[6], mk[7])));
+        };
+        if (t == 0) {  // the first keys set the reference maximum
+          float mk[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) mk[c] = x[c];
+#pragma unroll
+          for (int i = 8; i < kHalf; i += 8) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) mk[c] = fmaxf(mk[c], x[i + c]);
+          }
+          m_run = max8(mk) * sc;
+        }
+        // P = exp2(s*c - m_run), taken relative to the reference maximum m_run
+        // as it stands; the maximum of these keys is formed alongside.  A row
+        // without keys keeps the maximum -inf: all its P are 0.  P is rounded to
+        // bf16, as in the dense prefill: the remainders would be a second
+        // product (see extend_narrow.cu, where it is free).
+        float lsum = 0.f, t_mx = -INFINITY;
+        auto make_p = [&](bool with_max) {
+          const float mneg = m_run == -INFINITY ? 0.f : -m_run;
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+          float mk[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) mk[c] = -INFINITY;
+          uint32_t pk[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            x[i] = __uint_as_float(s0[i]);
-            x[32 + i] = __uint_as_float(s1[i]);
+            const float a0 = x[2 * i], a1 = x[2 * i + 1];
+            if (with_max) mk[i & 7] = fmaxf(mk[i & 7], fmaxf(a0, a1));
+            const float p0 = fast_exp2(fmaf(a0, sc, mneg));
+            const float p1 = fast_exp2(fmaf(a1, sc, mneg));
+            acc[i & 3] += p0 + p1;
+            pk[i] = pack_bf16x2(p0, p1);
           }
-          if (last < 64 * half + 63) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (64 * half + i > last) x[i] = -INFINITY;
-          }
-          auto max8 = [](const float (&mk)[8]) {
-            return fmaxf(fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])),
-                         fmaxf(fmaxf(mk[4], mk[5]), fmaxf(mk[6], mk[7])));
-          };
-          if (j == 0 && half == 0) {  // the first keys set the reference maximum
-            float mk[8];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) mk[c] = x[c];
-#pragma unroll
-            for (int i = 8; i < 64; i += 8) {
-#pragma unroll
-              for (int c = 0; c < 8; ++c) mk[c] = fmaxf(mk[c], x[i + c]);
-            }
-            m_run = max8(mk) * sc;
-          }
-          // P = exp2(s*c - m_run), taken relative to the reference maximum m_run as it stands; the
-          // maximum of these keys is formed alongside.  A row without keys keeps the maximum -inf:
-          // all its P are 0.  P is rounded to bf16, as in the dense prefill: the remainders would be
-          // a second product (see extend_narrow.cu, where it is free).
-          float lsum = 0.f, h_mx = -INFINITY;
-          auto make_p = [&](bool with_max) {
-            const float mneg = m_run == -INFINITY ? 0.f : -m_run;
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            float mk[8];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) mk[c] = -INFINITY;
-            uint32_t pk[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float a0 = x[2 * i], a1 = x[2 * i + 1];
-              if (with_max) mk[i & 7] = fmaxf(mk[i & 7], fmaxf(a0, a1));
-              const float p0 = fast_exp2(fmaf(a0, sc, mneg));
-              const float p1 = fast_exp2(fmaf(a1, sc, mneg));
-              acc[i & 3] += p0 + p1;
-              pk[i] = pack_bf16x2(p0, p1);
-            }
-            tmem_st32(t_s + 32 * half, pk);
-            lsum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-            if (with_max) h_mx = max8(mk) * sc;
-          };
-          make_p(true);
-          // A jump of the maximum by more than 2^64 would overflow P: take O (once the previous
-          // tile's PV has completed) and this tile's first half of P to the new maximum and redo
-          // these keys.
-          const bool hard = h_mx > m_run + kOverflowGuard;
-          if (__any_sync(0xffffffffu, hard)) {
-            tmem_st_wait();
-            const float alpha = hard ? fast_exp2(m_run - h_mx) : 1.0f;
-            if (j > 0) {
-              if (!(sm_ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[map], (g - 1) & 1, wc)))) break;
-              tc_fence_after();
-              rescale_o(alpha);
-            } else {
-              l_run *= alpha;
-            }
-            if (half) {
-              uint32_t pk[32];
-              tmem_ld32_sync(t_s, pk);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) pk[i] = pack_bf16x2(bf16lo_to_f32(pk[i]) * alpha, bf16hi_to_f32(pk[i]) * alpha);
-              tmem_st32(t_s, pk);
-            }
-            if (hard) m_run = h_mx;
-            make_p(false);
-          }
-          l_run += lsum;
-          t_mx = fmaxf(t_mx, h_mx);
+          tmem_st32(t_s + kHalf * b, pk);
+          lsum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+          if (with_max) t_mx = max8(mk) * sc;
+        };
+        make_p(true);
+        // A jump of the maximum by more than 2^64 would overflow P: rescale O
+        // to the new maximum (after the previous PV has completed) and redo P.
+        const bool hard = t > 0 && t_mx > m_run + kOverflowGuard;
+        if (__any_sync(0xffffffffu, hard)) {
+          tmem_st_wait();
+          if (!(sm_ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[map][(g - 1) & 1], ((g - 1) >> 1) & 1, wc)))) break;
+          tc_fence_after();
+          rescale_o(hard ? fast_exp2(m_run - t_mx) : 1.0f);
+          if (hard) m_run = t_mx;
+          make_p(false);
         }
-        if (!sm_ok) break;
+        l_run += lsum;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->p_full[map]);
+        if (lane == 0) mbar_arrive(&bars->p_full[map][b]);
         // Lazy rescale: keep the reference within 2^8 of the running maximum.
-        // O is rescaled once this tile's PV (which used the old reference) has completed.
+        // O is rescaled once this PV (which used the old reference) has completed.
         const bool need = t_mx > m_run + kRescaleThreshold;
         if (__any_sync(0xffffffffu, need)) {
-          if (!(sm_ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[map], g & 1, wc)))) break;
+          if (!(sm_ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[map][b], (g >> 1) & 1, wc)))) break;
           tc_fence_after();
           rescale_o(need ? fast_exp2(m_run - t_mx) : 1.0f);
           if (need) m_run = t_mx;
@@ -409,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // ------------------------------------------------------ epilogue --
       // O is complete once the segment's last PV (and with it every earlier MMA) has.
-      if (sm_ok) sm_ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[map], (g - 1) & 1, wc));
+      if (sm_ok) sm_ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[map][(g - 1) & 1], ((g - 1) >> 1) & 1, wc));
       tc_fence_after();
       if (!wk.whole()) {
         // a part of the row's keys: this map's sums to the worker's record
