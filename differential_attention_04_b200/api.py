@@ -41,17 +41,21 @@ def _ptr(t: torch.Tensor | None) -> int | None:
 
 def _dev(*ts: torch.Tensor) -> torch.device:
     """The one CUDA device all of `ts` live on (every tensor contiguous)."""
-    dev = None
+    dev = ts[0].device
+    for t in ts:
+        if t.device != dev or not t.is_contiguous():
+            break
+    else:
+        if dev.type == "cuda":
+            return dev
+    # something is wrong with them: the first fault, tensor by tensor
     for t in ts:
         if not t.is_cuda:
             raise ValueError("all tensors must be CUDA tensors")
         if not t.is_contiguous():
             raise ValueError("all tensors must be contiguous")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
+        if t.device != dev:
             raise ValueError(f"all tensors must be on one device (found {dev} and {t.device})")
-    return dev
 
 
 def _launch(name: str, tensors, *args) -> None:
@@ -498,6 +502,7 @@ def paged_step(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torc
     if pool_out is None:
         pool_out = pool
     _i32("pool_out", pool_out, 2)
+    ts = (ctx_lens, new_lens, block_table, free_pages, pool, pool_out)
     if out is None:  # parts of one allocation
         out = torch.unsafe_split_with_sizes(
             torch.empty(2 * S + 2 * T + 5, dtype=torch.int32, device=ctx_lens.device), (S + 1, S, T, T, 4))
@@ -505,8 +510,9 @@ def paged_step(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torc
         _need(len(out) == 5, "out must hold (cu_q, kv_lens, positions, slots, info)")
         for name, t, n in zip(("cu_q", "kv_lens", "positions", "slots", "info"), out, (S + 1, S, T, T, 4)):
             _i32(name, t, n)
+        ts += tuple(out)
     cu_q, kv_lens, positions, slots, info = out
-    _launch("diffattn_paged_step", (ctx_lens, new_lens, block_table, free_pages, pool, pool_out, *out),
+    _launch("diffattn_paged_step", ts,
             _ptr(ctx_lens), _ptr(new_lens), S, _ptr(block_table), max_pages, _ptr(free_pages), free_pages.numel(),
             _ptr(pool), _ptr(pool_out), int(page_size), T, _ptr(cu_q), _ptr(kv_lens), _ptr(positions), _ptr(slots),
             _ptr(info))

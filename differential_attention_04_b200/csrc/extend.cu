@@ -82,6 +82,9 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
   WideTile* wide = reinterpret_cast<WideTile*>(plan + lay.wide);
   long long* npre = reinterpret_cast<long long*>(plan + lay.narrow_pre);
   long long* wpre = reinterpret_cast<long long*>(plan + lay.wide_pre);
+  WideItem* items = reinterpret_cast<WideItem*>(plan + lay.items);
+  __shared__ long long cut[2][kNarrowWorkers + 1];  // where the workers' ranges begin on the lines
+  __shared__ int s_rounds;
   const int tid = threadIdx.x, lane = tid & 31;
   const int G = n.H / n.H_kv, tpt = kWideRows / G;
 
@@ -163,19 +166,67 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
     wpre[ntiles] = wunits;
   }
   __syncthreads();
-  // an item costs its units and kNarrowCost or wide_cost(n.d) more; a boundary inside those is one before its first unit
+  const int wc = wide_cost(n.d);
   const long long U[2] = {nunits + static_cast<long long>(nreqs) * n.H_kv * kNarrowCost,
-                          (wunits + static_cast<long long>(ntiles) * wide_cost(n.d)) * n.H_kv};
+                          (wunits + static_cast<long long>(ntiles) * wc) * n.H_kv};
   const int W[2] = {static_cast<int>(min(U[0], static_cast<long long>(kNarrowWorkers))),
                     static_cast<int>(min(U[1], static_cast<long long>(wide_workers(n.d))))};
-  if (tid == 0) *head = PlanHeader{{W[0], W[1]}, causal, ntiles, n, kPlanMagic, {}};
+  auto wide_line = [&](int k) { return wpre[k] + static_cast<long long>(k) * wc; };  // of one key head
+  // the wide items in order, and how many rounds of whole ones leave every worker at least one unit of its share
+  auto item_index = [&](const WideTile& t, int x, int hk) {
+    return static_cast<long long>(t.first) * n.H_kv + static_cast<long long>(hk) * t.count + (x - t.first);
+  };
+  for (int x = tid; x < ntiles; x += kPlanThreads) {
+    const WideTile t = wide[x];
+    for (int hk = 0; hk < n.H_kv; ++hk)
+      items[item_index(t, x, hk)] = WideItem{t.tok0, t.ntok, t.lim0, t.units, t.L, t.s, hk, x};
+  }
+  const long long nitems = static_cast<long long>(ntiles) * n.H_kv;
+  if (tid == 0) s_rounds = W[1] > 0 ? static_cast<int>(nitems / W[1]) : 0;
+  __syncthreads();
+  if (tid < W[1]) {
+    const long long most = U[1] / W[1] - 1;
+    long long sum = 0;
+    int r = 0;
+    for (; r < s_rounds; ++r) {  // (another worker may lower the bound meanwhile)
+      sum += items[static_cast<long long>(r) * W[1] + tid].units + wc;
+      if (sum > most) break;
+    }
+    atomicMin(&s_rounds, r);
+  }
+  __syncthreads();
+  const int rounds = s_rounds;
+  if (tid < W[1]) {
+    long long sum = 0;
+    for (int r = 0; r < rounds; ++r) sum += items[static_cast<long long>(r) * W[1] + tid].units + wc;
+    cut[1][tid] = sum;
+  }
+  if (tid < W[0]) cut[0][tid] = tid * U[0] / W[0];
+  __syncthreads();
+  if (tid == 0 && W[1] > 0) {
+    // the line behind the whole items, cut where the workers' shares are used up
+    long long at = U[1], used = 0;
+    const long long done = static_cast<long long>(rounds) * W[1];
+    if (done < nitems) {
+      const int x = items[done].tile, first = wide[x].first, cnt = wide[x].count;
+      at = wide_line(first) * n.H_kv + items[done].hk * (wide_line(first + cnt) - wide_line(first)) + wide_line(x) -
+           wide_line(first);
+    }
+    for (int w = 0; w < W[1]; ++w) {
+      const long long took = cut[1][w];
+      cut[1][w] = at + w * U[1] / W[1] - used;
+      used += took;
+    }
+  }
+  if (tid == 0) *head = PlanHeader{{W[0], W[1]}, causal, ntiles, n, kPlanMagic, rounds, {}};
+  __syncthreads();
   // the workers: where each begins, and the item that it leaves unfinished
   for (int i = tid; i < kNarrowWorkers + wide_workers(n.d); i += kPlanThreads) {
     const int c = i >= kNarrowWorkers, w = c ? i - kNarrowWorkers : i;
     WorkStart st{0, 0, 0, 0};
     WorkTail tl{0, 0, 0, 0};
     if (w < W[c]) {
-      const int ic = c ? wide_cost(n.d) : kNarrowCost;
+      const int ic = c ? wc : kNarrowCost;
       // the item at u on the line of costs, its first unit and the one behind its last (counted over all
       // items), and the unit of it that u means
       struct Spot {
@@ -194,7 +245,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
           r.b = npre[r.at] + r.hk * per;
           r.e = r.b + per;
         } else {
-          auto cost = [&](int k) { return wpre[k] + static_cast<long long>(k) * ic; };  // of one key head
+          auto cost = wide_line;
           const int any = last_at_most(0, ntiles - 1, u, [&](int k) { return cost(wide[k].first) * n.H_kv; });
           const int first = wide[any].first, cnt = wide[any].count;
           const long long c0 = cost(first), per = cost(first + cnt) - c0, off = u - c0 * n.H_kv;
@@ -208,19 +259,22 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
         r.unit = max(0ll, u - r.cost - ic);
         return r;
       };
-      const Spot x0 = spot(w * U[c] / W[c]);
-      const bool last = w + 1 == W[c];
-      const Spot x1 = last ? x0 : spot((w + 1) * U[c] / W[c]);
-      const long long u0 = x0.b + x0.unit, u1 = last ? (c ? wunits * n.H_kv : nunits) : x1.b + x1.unit;
-      if (u1 > u0) st = WorkStart{x0.at, x0.hk, static_cast<int>(x0.unit), static_cast<int>(u1 - u0)};
-      // The item that the range ends in is split if the next worker begins
-      // inside it (floor(v U / W) < x holds for v up to (x W - 1) / U).  Its
-      // owner is the last worker that begins at or before its first unit.
-      if (!last && x1.unit > 0) {
-        const int owner = static_cast<int>(((x1.cost + ic + 1) * W[c] - 1) / U[c]);
-        const int end = static_cast<int>(min(static_cast<long long>(W[c] - 1),
-                                             ((x1.cost + ic + x1.e - x1.b) * W[c] - 1) / U[c]));
-        if (end > w) tl = WorkTail{x1.at, x1.hk, end - owner + 1, w - owner};
+      const bool last = w + 1 == W[c], none = cut[c][w] >= U[c];
+      if (!none) {
+        const Spot x0 = spot(cut[c][w]);
+        const Spot x1 = last ? x0 : spot(min(cut[c][w + 1], U[c] - 1));
+        const long long all = c ? wunits * n.H_kv : nunits;
+        const long long u0 = x0.b + x0.unit, u1 = last || cut[c][w + 1] >= U[c] ? all : x1.b + x1.unit;
+        auto index = [&](const Spot& x) { return c ? static_cast<int>(item_index(wide[x.at], x.at, x.hk)) : x.at; };
+        if (u1 > u0) st = WorkStart{index(x0), x0.hk, static_cast<int>(x0.unit), static_cast<int>(u1 - u0)};
+        // The item that the range ends in is split if the next worker begins
+        // inside it.  Its owner is the last worker that begins at or before
+        // its first unit.
+        if (u1 < all && x1.unit > 0) {
+          const int owner = last_at_most(0, w, x1.cost + ic, [&](int v) { return cut[c][v]; });
+          const int end = last_at_most(w + 1, W[c] - 1, x1.cost + ic + x1.e - x1.b - 1, [&](int v) { return cut[c][v]; });
+          tl = WorkTail{index(x1), x1.hk, end - owner + 1, w - owner};
+        }
       }
     }
     reinterpret_cast<WorkStart*>(plan + lay.starts[c])[w] = st;

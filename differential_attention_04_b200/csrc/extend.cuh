@@ -7,14 +7,21 @@
 // up to 128 rows on the tensor cores).  An item is one (request, key head) of
 // the narrow class or one (row tile, key head) of the wide class; its work is
 // its number of units, blocks of kUnit keys that its last row can see (at
-// least one, so that rows without keys are written too).  The items of a class
-// lie end to end on a line of units, request by request, then key head by key
-// head, then row tile by row tile; worker w of W takes units
-// floor(w U / W) .. floor((w + 1) U / W) - 1.  So all workers get the same
-// work (to one unit) whatever the lengths, and only a worker's first and last
-// items can be split: their unnormalised sums go to the workspace records
-// 2 w (the item began before the worker's range) and 2 w + 1 (it began inside
-// it and goes on behind it), which the joining kernel adds up in order.
+// least one, so that rows without keys are written too), and a fixed number
+// more for what it costs once (the start of its pipeline, its epilogue).
+//
+// The items of a class are in order of requests, then key heads, then row
+// tiles, and lie end to end on a line of costs.  W workers get the same share
+// of it (to one unit) whatever the lengths:
+//   * Wide class only: in each of the first R rounds, worker w takes the whole
+//     item round * W + w.  So the row tiles of a key head run side by side and
+//     read its keys and values at about the same time, once from memory for
+//     all of them.  R is the most rounds that leave no worker above its share.
+//   * The rest of the line is cut where the workers' shares are used up.  Only
+//     a worker's first and last items there can be split: their unnormalised
+//     sums go to the workspace records 2 w (the item began before the worker's
+//     range) and 2 w + 1 (it began inside it and goes on behind it), which the
+//     joining kernel adds up in order.
 #pragma once
 
 #include "internal.h"
@@ -24,8 +31,12 @@ namespace diffattn {
 constexpr int kUnit = 128;
 constexpr int kNarrowRows = 8;
 constexpr int kWideRows = 128;
+// What an item costs beside its units, in units, from times of 74 requests of
+// 128 rows over 128 and 640 keys: 12 and 20 thousand cycles against 3.7 and 2.8
+// thousand a unit (ten ragged chunks and prompts, d = 128: 165 us with 3, 138
+// with 7).  A narrow item's end is hidden by the loads that run ahead.
 constexpr int kNarrowCost = 0;
-__host__ __device__ constexpr int wide_cost(int d) { return d == 64 ? 2 : 3; }
+__host__ __device__ constexpr int wide_cost(int d) { return d == 64 ? 3 : 7; }
 constexpr int kNarrowWorkers = 148;  // one CTA per SM
 // One CTA per SM (both maps), or one CTA pair per two SMs (a map each): two
 // output tiles of 2 d = 128 columns fit tensor memory, two of 256 do not.
@@ -36,7 +47,9 @@ struct PlanHeader {
   int causal;
   int tiles;           // entries of the list of row tiles
   ExtendShape shape;   // the sizes that the plan was made for
-  int magic, pad[5];
+  int magic;
+  int rounds;          // whole items of a wide worker
+  int pad[4];
 };
 constexpr int kPlanMagic = 0x64706c6e;
 constexpr int kMaxKeys = 0x7fffff00;  // keys of a request: a unit behind the last one still has a 32-bit index
@@ -45,24 +58,30 @@ static_assert(sizeof(PlanHeader) == 64, "the sections behind the header are 16-b
 struct NarrowReq {
   int q0, n, L, s;  // first row, new tokens, cached tokens, request
 };
-struct WideTile {
-  int tok0, ntok;       // its tokens' rows
-  int lim0;             // last key its first token sees (causal: one more per token)
-  int units;            // units per key head
-  int L, s, first, count;  // cached tokens, request; the request's first row tile and their number
+struct WideTile {  // a row tile, while the schedule is made
+  int tok0, ntok, lim0, units;
+  int L, s, first, count;  // first row tile of its request and their number
 };
-// Where a worker begins: item (at, hk), its unit, and how many units it takes.
-// Its tail: the split item (at, hk) that its range ends in and that goes on
-// behind it, in how many parts (0: there is none), and which of them it has.
+struct WideItem {
+  int tok0, ntok;  // its tokens' rows
+  int lim0;        // last key its first token sees (causal: one more per token)
+  int units;
+  int L, s, hk;    // cached tokens, request, key head
+  int tile;        // in the schedule's list of row tiles
+};
+// Where a worker's range begins: item (list index, and key head of a narrow
+// one), its unit, and how many units it takes.
 struct WorkStart {
   int at, hk, unit, count;
 };
+// The split item that the range ends in and that goes on behind it, in how
+// many parts (0: there is none), and which of them the worker has.
 struct WorkTail {
   int at, hk, parts, member;
 };
 
 struct PlanLayout {
-  size_t starts[2], tails[2], narrow, narrow_pre, wide, wide_pre, bytes;
+  size_t starts[2], tails[2], narrow, narrow_pre, wide, wide_pre, items, bytes;
   int max_tiles;  // row tiles of the wide class there can be
 };
 
@@ -90,6 +109,9 @@ __host__ __device__ inline PlanLayout plan_layout(const ExtendShape& n) {
   at += (static_cast<size_t>(n.S) + 1) * sizeof(long long);
   l.wide_pre = at;
   at += (static_cast<size_t>(l.max_tiles) + 1) * sizeof(long long);
+  at = (at + 15) & ~static_cast<size_t>(15);
+  l.items = at;
+  at += static_cast<size_t>(l.max_tiles) * n.H_kv * sizeof(WideItem);
   l.bytes = (at + 15) & ~static_cast<size_t>(15);
   return l;
 }
@@ -104,7 +126,7 @@ struct PlanView {
   const WorkStart* starts;
   const WorkTail* tails;
   const NarrowReq* narrow;
-  const WideTile* wide;
+  const WideItem* wide;
 };
 // Whether the buffer holds a plan of these sizes; the kernels do nothing otherwise.
 __device__ inline bool plan_fits(const void* plan, const ExtendShape& n, int* status) {
@@ -120,7 +142,7 @@ __device__ inline PlanView plan_view(const void* plan, const ExtendShape& n, int
   const char* p = static_cast<const char*>(plan);
   return PlanView{reinterpret_cast<const PlanHeader*>(p), reinterpret_cast<const WorkStart*>(p + l.starts[cls]),
                   reinterpret_cast<const WorkTail*>(p + l.tails[cls]),
-                  reinterpret_cast<const NarrowReq*>(p + l.narrow), reinterpret_cast<const WideTile*>(p + l.wide)};
+                  reinterpret_cast<const NarrowReq*>(p + l.narrow), reinterpret_cast<const WideItem*>(p + l.items)};
 }
 
 cudaError_t launch_extend_narrow(const ExtendArgs& a, float* recs, DevCtl ctl, cudaStream_t stream);

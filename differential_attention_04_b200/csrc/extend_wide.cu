@@ -84,17 +84,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!plan_fits(p.plan, p.n, p.status)) return;  // the same for both CTAs of the cluster
   const PlanView pv = plan_view(p.plan, p.n, 1);
   Walk wk;
-  {
-    const WorkStart st = pv.starts[blockIdx.x >> 1];
-    if (st.count == 0) return;  // and this too
-    wk.at = st.at;
-    wk.hk = st.hk;
-    wk.unit = st.unit;
-    wk.left = st.count;
-    wk.open(pv.wide);
-  }
+  if (!wk.begin(pv, blockIdx.x >> 1)) return;  // and this too
   const int causal = pv.head->causal;
-  const int H = p.n.H, H_kv = p.n.H_kv, G = H / H_kv, tpt = kBM / G;
+  const int H = p.n.H, G = H / p.n.H_kv, tpt = kBM / G;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem + C::OFF_Q;
@@ -170,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_expect_tx(&bars->q_full, G * tpt * 128 * C::QBLK);
 #pragma unroll
         for (int blk = 0; blk < C::QBLK; ++blk)
-          tma_load_4d(sQ + blk * C::BLK_BYTES, &tq, &bars->q_full, blk * 64, static_cast<int>(rank), wk.hk * G,
+          tma_load_4d(sQ + blk * C::BLK_BYTES, &tq, &bars->q_full, blk * 64, static_cast<int>(rank), wk.t.hk * G,
                       wk.t.tok0);
       }
       for (int j = 0; j < wk.take; ++j, ++gk) {
@@ -183,10 +175,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int blk = 0; blk < C::QBLK; ++blk)
             tma_load_4d(sK + st * C::K_BYTES + blk * C::BLK_BYTES + lane * box.rows * 128, &tk, &bars->k_full[st],
-                        blk * 64, 2 * wk.hk + static_cast<int>(rank), row, 0);
+                        blk * 64, 2 * wk.t.hk + static_cast<int>(rank), row, 0);
         }
       }
-      if (!ok || !wk.next(pv.wide, H_kv)) break;
+      if (!ok || !wk.next(pv)) break;
     }
     // nothing may still be landing in shared memory when the CTA exits
     for (int j = max(0, gk - 2); j < gk; ++j) mbar_wait(&bars->k_full[j & 1], (j >> 1) & 1, wdrain);
@@ -211,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane < boxes) {
 #pragma unroll
           for (int blk = 0; blk < C::VBLK; ++blk)
-            tma_load_4d(dst + blk * C::BLK_BYTES + lane * box.rows * 128, &tv, bar, blk * 64, wk.hk, row, 0);
+            tma_load_4d(dst + blk * C::BLK_BYTES + lane * box.rows * 128, &tv, bar, blk * 64, wk.t.hk, row, 0);
         }
         if (!full) {
           mbar_wait(&bars->v_land, ragged & 1, wdrain);
@@ -220,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&bars->v_full[st]);
         }
       }
-      if (!ok || !wk.next(pv.wide, H_kv)) break;
+      if (!ok || !wk.next(pv)) break;
     }
     for (int j = max(0, gv - 2); j < gv; ++j) mbar_wait(&bars->v_full[j & 1], (j >> 1) & 1, wdrain);
     __syncwarp();
@@ -273,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j > 0) ok = issue_pv(j == 1);
         }
         if (ok) ok = issue_pv(wk.take == 1);
-        if (!ok || !wk.next(pv.wide, H_kv)) break;
+        if (!ok || !wk.next(pv)) break;
       }
       // drain: every issued MMA has completed before tensor memory is read or freed
       umma_commit(&bars->mma_done);
@@ -299,14 +291,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                        : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
                        : "r"(tile + blk * C::BLK_BYTES + r * 128 + ((chunk ^ (r & 7)) << 4))
                        : "memory");
-          const size_t row = static_cast<size_t>(wk.t.tok0 + r / G) * H + wk.hk * G + r % G;
+          const size_t row = static_cast<size_t>(wk.t.tok0 + r / G) * H + wk.t.hk * G + r % G;
           *reinterpret_cast<uint4*>(p.o + row * C::DV + own0 + 64 * blk + 8 * chunk) =
               make_uint4(x[0], x[1], x[2], x[3]);
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->epi_free);
-    } while (wk.next(pv.wide, H_kv));
+    } while (wk.next(pv));
   }
 
   if (warp >= 4) {
@@ -542,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // hand the staged tile to warp 3, which copies it out and frees the V
       // stages, and go on with the next segment
       named_bar_arrive(2, 160);
-    } while (wk.next(pv.wide, H_kv));
+    } while (wk.next(pv));
   }
 
   tc_fence_before();

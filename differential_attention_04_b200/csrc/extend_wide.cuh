@@ -30,26 +30,51 @@ struct WideParams {
   unsigned long long limit_ns;
 };
 
-// A worker's walk over its segments: units unit .. unit + take - 1 of (row tile at, key head hk).
+// A worker's walk over its segments: units unit .. unit + take - 1 of an item,
+// first its whole items (every workers-th up to `whole_end`), then its range of
+// the line.
 struct Walk {
-  WideTile t;
-  int at, hk, unit, take, left;
-  __device__ void open(const WideTile* list) {
-    t = list[at];
-    take = min(left, t.units - unit);
+  WideItem t;
+  int at, unit, take, left;  // left: units of the range from this segment on
+  int worker, workers, whole_end;
+  __device__ bool begin(const PlanView& pv, int w) {  // false: there is no work
+    worker = w;
+    workers = pv.head->workers[1];
+    whole_end = pv.head->rounds * workers;
+    left = pv.starts[w].count;
+    if (w >= workers || whole_end == 0) return open_range(pv);
+    at = w;
+    open_whole(pv);
+    return true;
   }
-  __device__ bool next(const WideTile* list, int H_kv) {  // false: the range is done
+  __device__ void open_whole(const PlanView& pv) {
+    t = pv.wide[at];
+    unit = 0;
+    take = t.units;
+  }
+  __device__ bool open_range(const PlanView& pv) {
+    whole_end = 0;
+    if (left <= 0) return false;
+    const WorkStart st = pv.starts[worker];
+    at = st.at;
+    unit = st.unit;
+    t = pv.wide[at];
+    take = min(left, t.units - unit);
+    return true;
+  }
+  __device__ bool next(const PlanView& pv) {  // false: that was the last segment
+    if (whole_end) {
+      at += workers;
+      if (at >= whole_end) return open_range(pv);
+      open_whole(pv);
+      return true;
+    }
     left -= take;
     if (left <= 0) return false;
+    ++at;
+    t = pv.wide[at];
     unit = 0;
-    if (++at == t.first + t.count) {
-      if (++hk < H_kv) {
-        at = t.first;
-      } else {
-        hk = 0;
-      }
-    }
-    open(list);
+    take = min(left, t.units);
     return true;
   }
   __device__ bool begins() const { return unit == 0; }
@@ -62,7 +87,7 @@ struct TileBoxes {
   int rows, shift;
   __device__ explicit TileBoxes(const WideParams& p) : rows(min(1 << p.page_shift, kUnit)), shift(min(p.page_shift, 7)) {}
   __device__ int count(int key0, int L) const { return L <= key0 ? 0 : (min(kUnit, L - key0) + rows - 1) >> shift; }
-  __device__ int row(const WideParams& p, const WideTile& t, int key0, int boxes, int lane) const {
+  __device__ int row(const WideParams& p, const WideItem& t, int key0, int boxes, int lane) const {
     if (lane >= boxes) return 0;
     const int key = key0 + (lane << shift);
     const int page = p.block_table[static_cast<size_t>(t.s) * p.max_pages + (key >> p.page_shift)];

@@ -86,17 +86,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!plan_fits(p.plan, p.n, p.status)) return;
   const PlanView pv = plan_view(p.plan, p.n, 1);
   Walk wk;
-  {
-    const WorkStart st = pv.starts[blockIdx.x];
-    if (st.count == 0) return;
-    wk.at = st.at;
-    wk.hk = st.hk;
-    wk.unit = st.unit;
-    wk.left = st.count;
-    wk.open(pv.wide);
-  }
+  if (!wk.begin(pv, blockIdx.x)) return;
   const int causal = pv.head->causal;
-  const int H = p.n.H, H_kv = p.n.H_kv, G = H / H_kv, tpt = kBM / G;
+  const int H = p.n.H, G = H / p.n.H_kv, tpt = kBM / G;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023) {  // the swizzled tiles need it; there is no room to align by hand
     if (threadIdx.x == 0) atomicCAS(p.status, 0, 6);
@@ -155,126 +147,130 @@ __global__ void __launch_bounds__(kThreads, 1)
   const WaitCtl wdrain{p.status, &drain_abort, 1000000000ull};
   const TileBoxes box(p);
 
-  if (warp == 0) {
-    // ---------------------------------------------------- Q / K producer --
-    int gk = 0;  // K tiles issued
-    bool ok = true;
-    for (int k = 0; ok; ++k) {
-      const int L = min(wk.t.L, p.max_keys);
-      if (wk.t.L > p.max_keys && lane == 0) atomicCAS(p.status, 0, 6);
-      // Q of this segment replaces the last one's once that one's S products have read it
-      if (k > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (k - 1) & 1, wc)))) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bars->q_full, 2 * G * tpt * 128);
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-          tma_load_4d(sQ + m * C::MAP_BYTES, &tq, &bars->q_full, 0, m, wk.hk * G, wk.t.tok0);
-      }
-      for (int j = 0; j < wk.take; ++j, ++gk) {
-        const int st = gk & 1, key0 = (wk.unit + j) * kBN;
-        const int boxes = box.count(key0, L), row = box.row(p, wk.t, key0, boxes, lane);
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_empty[st], ((gk >> 1) & 1) ^ 1, wc)))) break;
-        if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[st], 2 * boxes * box.rows * 128);
-        __syncwarp();
-        if (lane < boxes) {
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-            tma_load_4d(sK + (2 * st + m) * C::MAP_BYTES + lane * box.rows * 128, &tk, &bars->k_full[st], 0,
-                        2 * wk.hk + m, row, 0);
-        }
-      }
-      if (!ok || !wk.next(pv.wide, H_kv)) break;
-    }
-    // nothing may still be landing in shared memory when the CTA exits
-    for (int j = max(0, gk - 2); j < gk; ++j) mbar_wait(&bars->k_full[j & 1], (j >> 1) & 1, wdrain);
-    __syncwarp();
-  } else if (warp == 2) {
-    // -------------------------------------------------------- V producer --
-    int gv = 0, ragged = 0;  // V tiles issued; ragged ones among them
-    bool ok = true;
-    while (ok) {
-      const int L = min(wk.t.L, p.max_keys);
-      for (int j = 0; j < wk.take; ++j, ++gv) {
-        const int st = gv & 1, key0 = (wk.unit + j) * kBN;
-        const int boxes = box.count(key0, L), row = box.row(p, wk.t, key0, boxes, lane);
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_empty[st], ((gv >> 1) & 1) ^ 1, wc)))) break;
-        const bool full = key0 + kBN <= L;
-        uint64_t* bar = full ? &bars->v_full[st] : &bars->v_land;
-        uint8_t* dst = sV + st * C::V_BYTES;
-        if (lane == 0) mbar_arrive_expect_tx(bar, boxes * box.rows * 128 * C::VBLK);
-        __syncwarp();
-        if (lane < boxes) {
-#pragma unroll
-          for (int blk = 0; blk < C::VBLK; ++blk)
-            tma_load_4d(dst + blk * C::BLK_BYTES + lane * box.rows * 128, &tv, bar, blk * 64, wk.hk, row, 0);
-        }
-        if (!full) {
-          mbar_wait(&bars->v_land, ragged & 1, wdrain);
-          ++ragged;
-          clear_v_rows(dst, C::VBLK, max(0, L - key0), lane);
-          if (lane == 0) mbar_arrive(&bars->v_full[st]);
-        }
-      }
-      if (!ok || !wk.next(pv.wide, H_kv)) break;
-    }
-    for (int j = max(0, gv - 2); j < gv; ++j) mbar_wait(&bars->v_full[j & 1], (j >> 1) & 1, wdrain);
-    __syncwarp();
-  } else if (warp == 1 || warp == 3) {
-    // ------------------------------------- MMA issuers, one for each map --
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(128, kHalf, false, false);
-      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, C::DV, false, true);
-      const int m = warp >> 1;
-      const uint32_t sQa = smem_u32(sQ) + m * C::MAP_BYTES, sKa = smem_u32(sK) + m * C::MAP_BYTES, sVa = smem_u32(sV);
-      const uint32_t t_s = tmem + C::TM_S + 128 * m, t_o = tmem + C::TM_O + 128 * m;
-      int gs = 0;  // halves of tiles whose S products have been issued
-      int gp = 0;  // and whose PV products have
-      // S for half gs & 1 of tile gs / 2
-      auto issue_s = [&](bool last) -> bool {
-        const int st = (gs >> 1) & 1, b = gs & 1;
-        if (b == 0 && !mbar_wait(&bars->k_full[st], (gs >> 2) & 1, wc)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)  // each instruction takes 32 bytes of every row
-          umma_ss(t_s + kHalf * b, smem_desc_sw128(sQa + kk * 32, 16, 1024),
-                  smem_desc_sw128(sKa + 2 * st * C::MAP_BYTES + b * kHalf * 128 + kk * 32, 16, 1024), idesc_s,
-                  kk > 0 ? 1u : 0u);
-        umma_commit(&bars->s_full[m][b]);
-        if (b == 1) umma_commit(&bars->k_empty[st]);
-        if (last) umma_commit(&bars->q_empty);
-        ++gs;
-        return true;
-      };
+  // The block's 384 x 168 registers, split anew as 128 x 40 + 256 x 232 (short
+  // prompts: 131 us against 147).
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0) {
+      // ---------------------------------------------------- Q / K producer --
+      int gk = 0;  // K tiles issued
       bool ok = true;
       for (int k = 0; ok; ++k) {
-        const int n = 2 * wk.take;
-        ok = mbar_wait(&bars->q_full, k & 1, wc) && issue_s(false);
-        for (int t = 0; ok && t < n; ++t, ++gp) {
-          if (t + 1 < n && !(ok = issue_s(t + 2 == n))) break;
-          const int st = (gp >> 1) & 1, b = gp & 1;
-          if (!(ok = mbar_wait(&bars->p_full[m][b], (gp >> 1) & 1, wc))) break;
-          if (b == 0 && !(ok = mbar_wait(&bars->v_full[st], (gp >> 2) & 1, wc))) break;
-          // a new segment's O replaces the last one's once that has been read
-          if (t == 0 && k > 0 && !(ok = mbar_wait(&bars->o_free[m], (k - 1) & 1, wc))) break;
+        const int L = min(wk.t.L, p.max_keys);
+        if (wk.t.L > p.max_keys && lane == 0) atomicCAS(p.status, 0, 6);
+        // Q of this segment replaces the last one's once that one's S products have read it
+        if (k > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (k - 1) & 1, wc)))) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->q_full, 2 * G * tpt * 128);
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            tma_load_4d(sQ + m * C::MAP_BYTES, &tq, &bars->q_full, 0, m, wk.t.hk * G, wk.t.tok0);
+        }
+        for (int j = 0; j < wk.take; ++j, ++gk) {
+          const int st = gk & 1, key0 = (wk.unit + j) * kBN;
+          const int boxes = box.count(key0, L), row = box.row(p, wk.t, key0, boxes, lane);
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_empty[st], ((gk >> 1) & 1) ^ 1, wc)))) break;
+          if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[st], 2 * boxes * box.rows * 128);
+          __syncwarp();
+          if (lane < boxes) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+              tma_load_4d(sK + (2 * st + m) * C::MAP_BYTES + lane * box.rows * 128, &tk, &bars->k_full[st], 0,
+                          2 * wk.t.hk + m, row, 0);
+          }
+        }
+        if (!ok || !wk.next(pv)) break;
+      }
+      // nothing may still be landing in shared memory when the CTA exits
+      for (int j = max(0, gk - 2); j < gk; ++j) mbar_wait(&bars->k_full[j & 1], (j >> 1) & 1, wdrain);
+      __syncwarp();
+    } else if (warp == 2) {
+      // -------------------------------------------------------- V producer --
+      int gv = 0, ragged = 0;  // V tiles issued; ragged ones among them
+      bool ok = true;
+      while (ok) {
+        const int L = min(wk.t.L, p.max_keys);
+        for (int j = 0; j < wk.take; ++j, ++gv) {
+          const int st = gv & 1, key0 = (wk.unit + j) * kBN;
+          const int boxes = box.count(key0, L), row = box.row(p, wk.t, key0, boxes, lane);
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_empty[st], ((gv >> 1) & 1) ^ 1, wc)))) break;
+          const bool full = key0 + kBN <= L;
+          uint64_t* bar = full ? &bars->v_full[st] : &bars->v_land;
+          uint8_t* dst = sV + st * C::V_BYTES;
+          if (lane == 0) mbar_arrive_expect_tx(bar, boxes * box.rows * 128 * C::VBLK);
+          __syncwarp();
+          if (lane < boxes) {
+#pragma unroll
+            for (int blk = 0; blk < C::VBLK; ++blk)
+              tma_load_4d(dst + blk * C::BLK_BYTES + lane * box.rows * 128, &tv, bar, blk * 64, wk.t.hk, row, 0);
+          }
+          if (!full) {
+            mbar_wait(&bars->v_land, ragged & 1, wdrain);
+            ++ragged;
+            clear_v_rows(dst, C::VBLK, max(0, L - key0), lane);
+            if (lane == 0) mbar_arrive(&bars->v_full[st]);
+          }
+        }
+        if (!ok || !wk.next(pv)) break;
+      }
+      for (int j = max(0, gv - 2); j < gv; ++j) mbar_wait(&bars->v_full[j & 1], (j >> 1) & 1, wdrain);
+      __syncwarp();
+    } else if (warp == 1 || warp == 3) {
+      // ------------------------------------- MMA issuers, one for each map --
+      if (lane == 0) {
+        constexpr uint32_t idesc_s = idesc_bf16_f32(128, kHalf, false, false);
+        constexpr uint32_t idesc_pv = idesc_bf16_f32(128, C::DV, false, true);
+        const int m = warp >> 1;
+        const uint32_t sQa = smem_u32(sQ) + m * C::MAP_BYTES, sKa = smem_u32(sK) + m * C::MAP_BYTES, sVa = smem_u32(sV);
+        const uint32_t t_s = tmem + C::TM_S + 128 * m, t_o = tmem + C::TM_O + 128 * m;
+        int gs = 0;  // halves of tiles whose S products have been issued
+        int gp = 0;  // and whose PV products have
+        // S for half gs & 1 of tile gs / 2
+        auto issue_s = [&](bool last) -> bool {
+          const int st = (gs >> 1) & 1, b = gs & 1;
+          if (b == 0 && !mbar_wait(&bars->k_full[st], (gs >> 2) & 1, wc)) return false;
           tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < kHalf / 16; ++kk)
-            umma_ts(t_o, t_s + kHalf * b + 8 * kk,
-                    smem_desc_sw128(sVa + st * C::V_BYTES + (b * (kHalf / 16) + kk) * 2048, C::BLK_BYTES, 1024),
-                    idesc_pv, (t > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(&bars->pv_done[m][b]);
-          if (b == 1) umma_commit(&bars->v_empty[st]);
+          for (int kk = 0; kk < D / 16; ++kk)  // each instruction takes 32 bytes of every row
+            umma_ss(t_s + kHalf * b, smem_desc_sw128(sQa + kk * 32, 16, 1024),
+                    smem_desc_sw128(sKa + 2 * st * C::MAP_BYTES + b * kHalf * 128 + kk * 32, 16, 1024), idesc_s,
+                    kk > 0 ? 1u : 0u);
+          umma_commit(&bars->s_full[m][b]);
+          if (b == 1) umma_commit(&bars->k_empty[st]);
+          if (last) umma_commit(&bars->q_empty);
+          ++gs;
+          return true;
+        };
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+          const int n = 2 * wk.take;
+          ok = mbar_wait(&bars->q_full, k & 1, wc) && issue_s(false);
+          for (int t = 0; ok && t < n; ++t, ++gp) {
+            if (t + 1 < n && !(ok = issue_s(t + 2 == n))) break;
+            const int st = (gp >> 1) & 1, b = gp & 1;
+            if (!(ok = mbar_wait(&bars->p_full[m][b], (gp >> 1) & 1, wc))) break;
+            if (b == 0 && !(ok = mbar_wait(&bars->v_full[st], (gp >> 2) & 1, wc))) break;
+            // a new segment's O replaces the last one's once that has been read
+            if (t == 0 && k > 0 && !(ok = mbar_wait(&bars->o_free[m], (k - 1) & 1, wc))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < kHalf / 16; ++kk)
+              umma_ts(t_o, t_s + kHalf * b + 8 * kk,
+                      smem_desc_sw128(sVa + st * C::V_BYTES + (b * (kHalf / 16) + kk) * 2048, C::BLK_BYTES, 1024),
+                      idesc_pv, (t > 0 || kk > 0) ? 1u : 0u);
+            umma_commit(&bars->pv_done[m][b]);
+            if (b == 1) umma_commit(&bars->v_empty[st]);
+          }
+          if (!ok || !wk.next(pv)) break;
         }
-        if (!ok || !wk.next(pv.wide, H_kv)) break;
+        // drain: every issued MMA has completed before tensor memory is read or freed
+        umma_commit(&bars->mma_done);
+        mbar_wait(&bars->mma_done, 0, wdrain);
       }
-      // drain: every issued MMA has completed before tensor memory is read or freed
-      umma_commit(&bars->mma_done);
-      mbar_wait(&bars->mma_done, 0, wdrain);
+      __syncwarp();
     }
-    __syncwarp();
-  }
-
-  if (warp >= 4) {
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     // ------------------------------------------------ softmax + epilogue --
     const int quarter = warp & 3, map = (warp >> 2) - 1;
     const int r = quarter * 32 + lane;  // query row within the tile (= TMEM lane)
@@ -482,12 +478,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                      : "r"(out + lr * 128 + ((chunk ^ (lr & 7)) << 4))
                      : "memory");
         if (row < wk.t.ntok * G) {
-          const size_t at = static_cast<size_t>(wk.t.tok0 + row / G) * H + wk.hk * G + row % G;
+          const size_t at = static_cast<size_t>(wk.t.tok0 + row / G) * H + wk.t.hk * G + row % G;
           *reinterpret_cast<uint4*>(p.o + at * C::DV + map * D + 8 * chunk) = make_uint4(v[0], v[1], v[2], v[3]);
         }
       }
       __syncwarp();  // the buffer is read before the next segment's sums replace it
-    } while (wk.next(pv.wide, H_kv));
+    } while (wk.next(pv));
   }
 
   tc_fence_before();
