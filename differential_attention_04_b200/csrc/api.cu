@@ -137,8 +137,7 @@ bool encode_uncached(CUtensorMap* m, const MapKey& k) {
 size_t map_slot(const MapKey& k) {
   uint64_t h = reinterpret_cast<uintptr_t>(k.base) * 0x9E3779B97F4A7C15ull;
   for (int i = 0; i < 4; ++i) h = (h ^ k.d[i]) * 0x100000001B3ull;
-  h ^= static_cast<uint64_t>(k.kind) * 31 + static_cast<uint64_t>(k.box_rows) +
-       (static_cast<uint64_t>(k.box_outer - 1) << 16);
+  h ^= static_cast<uint64_t>(k.kind) * 31 + static_cast<uint64_t>(k.box_rows);
   return static_cast<size_t>((h >> 29) % (kMapSlots / 2)) * 2;
 }
 
@@ -163,11 +162,11 @@ bool encode_cached(CUtensorMap* m, const MapKey& k) {
 }
 
 // 4-D map over a row-major tensor with dims (innermost first) d0..d3 of bf16
-// (esize 2) or byte (esize 1) elements; box = 128 bytes x 1 x box_rows x
-// box_outer, 128-byte swizzle, zero fill out of bounds.
+// (esize 2) or byte (esize 1) elements; box = 128 bytes x 1 x box_rows x 1,
+// 128-byte swizzle, zero fill out of bounds.
 bool encode_4d(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t d3,
-               int esize = 2, int box_rows = 128, int box_outer = 1) {
-  return encode_cached(m, MapKey{base, {d0, d1, d2, d3}, esize, box_rows, box_outer});
+               int esize = 2, int box_rows = 128) {
+  return encode_cached(m, MapKey{base, {d0, d1, d2, d3}, esize, box_rows});
 }
 
 // 4-D map over packed e2m1 codes, dims (innermost first) d0 codes (two per
@@ -763,8 +762,10 @@ int diffattn_extend(const void* q, const void* k_cache, const void* v_cache, con
   if (extend_wide_possible(a.n)) {
     const uint64_t slots = static_cast<uint64_t>(num_pages) * page_size, kv = static_cast<uint64_t>(H_kv);
     const int G = H / H_kv, rows = page_size < 128 ? page_size : 128;
-    if (!encode_4d(&a.tq, q, d, 2, H, T, 2, G, 128 / G) || !encode_4d(&a.tk, k_cache, d, 2 * kv, slots, 1, 2, rows) ||
-        !encode_4d(&a.tv, v_cache, 2 * d, kv, slots, 1, 2, rows))
+    if (!encode_uncached(&a.tq, MapKey{q, {static_cast<uint64_t>(d), 2, static_cast<uint64_t>(H),
+                                           static_cast<uint64_t>(T)}, 2, G, 128 / G}) ||
+        !encode_uncached(&a.tk, MapKey{k_cache, {static_cast<uint64_t>(d), 2 * kv, slots, 1}, 2, rows}) ||
+        !encode_uncached(&a.tv, MapKey{v_cache, {2 * static_cast<uint64_t>(d), kv, slots, 1}, 2, rows}))
       return DIFFATTN_ERR_CUDA;
   }
   DevCtl ctl;

@@ -184,22 +184,36 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
   const long long nitems = static_cast<long long>(ntiles) * n.H_kv;
   if (tid == 0) s_rounds = W[1] > 0 ? static_cast<int>(nitems / W[1]) : 0;
   __syncthreads();
-  if (tid < W[1]) {
-    const long long most = U[1] / W[1] - 1;
-    long long sum = 0;
+  // A worker's whole items of rounds 0 .. limit - 1 while they cost at most `most`: their number, and their cost.
+  auto whole_items = [&](int limit, long long most, long long& cost) {
+    cost = 0;
     int r = 0;
-    for (; r < s_rounds; ++r) {  // (another worker may lower the bound meanwhile)
-      sum += items[static_cast<long long>(r) * W[1] + tid].units + wc;
-      if (sum > most) break;
+    while (r < limit) {
+      int u[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] = r + i < limit ? items[static_cast<long long>(r + i) * W[1] + tid].units : 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (r < limit) {
+          if (cost + u[i] + wc > most) return r;
+          cost += u[i] + wc;
+          ++r;
+        }
+      }
     }
+    return r;
+  };
+  if (tid < W[1]) {
+    long long cost;
+    const int r = whole_items(static_cast<int>(nitems / W[1]), U[1] / W[1] - 1, cost);
     atomicMin(&s_rounds, r);
   }
   __syncthreads();
   const int rounds = s_rounds;
   if (tid < W[1]) {
-    long long sum = 0;
-    for (int r = 0; r < rounds; ++r) sum += items[static_cast<long long>(r) * W[1] + tid].units + wc;
-    cut[1][tid] = sum;
+    long long cost;
+    whole_items(rounds, U[1], cost);
+    cut[1][tid] = cost;
   }
   if (tid < W[0]) cut[0][tid] = tid * U[0] / W[0];
   __syncthreads();

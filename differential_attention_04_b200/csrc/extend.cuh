@@ -92,7 +92,7 @@ __host__ __device__ inline bool wide_possible(const ExtendShape& n) {
 __host__ __device__ inline PlanLayout plan_layout(const ExtendShape& n) {
   PlanLayout l;
   const int tpt = kWideRows / (n.H / n.H_kv);
-  l.max_tiles = wide_possible(n) ? n.T / tpt + n.S : 0;
+  l.max_tiles = wide_possible(n) ? n.T / tpt + (n.S < n.T ? n.S : n.T) : 0;  // a request has a token at least
   size_t at = sizeof(PlanHeader);
   const int workers[2] = {kNarrowWorkers, wide_workers(n.d)};
   for (int c = 0; c < 2; ++c) {

@@ -457,6 +457,84 @@ def test_extend_offsets_behind_32_bits():
         _check(out, q, *small, np.where(table >= 0, table - first, -1), cu, kv, float(lam), w)
 
 
+def _check_on_device(got, q, kc, vc, table, cu, kv, lam, w, causal, li=0.4):
+    """The oracle's formulas and its bound in float64 torch on the device, for sizes where numpy takes too long."""
+    H, d, page, Hkv = q.shape[1], q.shape[3], kc.shape[1], kc.shape[2]
+    G = H // Hkv
+    for s, L in enumerate(kv):
+        a, b = int(cu[s]), int(cu[s + 1])
+        n = b - a
+        if n == 0:
+            continue
+        ids = torch.as_tensor(table[s, :-(-L // page)], device=DEV).long()
+        k, v = kc[ids].view(-1, Hkv, 2, d)[:L].double(), vc[ids].view(-1, Hkv, 2 * d)[:L].double()
+        see = torch.arange(L, device=DEV)[None] <= (torch.arange(n, device=DEV)[:, None] + (L - n) if causal else L)
+        for h in range(H):
+            o = e = 0.0
+            for m, c in ((0, 1.0), (1, -lam)):
+                x = (q[a:b, h, m].double() @ k[:, h // G, m].T / d ** 0.5).masked_fill(~see, -torch.inf)
+                p = torch.softmax(x, -1)
+                o, e = o + c * p @ v[:, h // G], e + P_ERR * abs(c) * p @ v[:, h // G].abs()
+            rms = ((o * o).mean(-1, keepdim=True) + 1e-5).sqrt()
+            ne = (e * e).mean(-1, keepdim=True).sqrt()
+            y = (1 - li) * w.double() * o / rms
+            tol = ((1 - li) * w.double()).abs() * (e + o.abs() * ne / rms) / rms / (1 - ne / rms)
+            tol = tol + OUT_ERR * (y.abs() + tol) + FLOOR
+            err = (got[a:b, h].double() - y).abs()
+            assert bool((err <= tol).all()), (s, h, float((err - tol).max()))
+
+
+@pytest.mark.parametrize("d,new,kv,H,Hkv,page,causal", [
+    (64, [1500], [1700], 32, 32, 16, True),        # whole items in rounds, then split ones
+    (128, [1000, 400, 1], [1000, 5000, 700], 16, 16, 64, True),
+    (128, [600, 0, 300, 7], [2500, 40, 300, 900], 24, 4, 256, True),
+    (64, [129] * 40, [129] * 40, 8, 8, 128, True),  # two tiles of one unit and two
+    (128, [260, 512], [3000, 512], 10, 10, 32, False),
+    (64, [40] * 9 + [1] * 9, [777] * 18, 14, 2, 16, True),
+    (128, [8, 1, 4, 5], [20000, 9000, 131, 64], 4, 4, 64, True)])
+def test_extend_larger(d, new, kv, H, Hkv, page, causal):
+    cu = np.concatenate([[0], np.cumsum(new)])
+    q, kc, vc, table = _cache(17, kv, H, Hkv, d, page, int(cu[-1]), garbage=float("nan"))
+    lam, w = torch.tensor([0.3], device=DEV), torch.linspace(0.5, 1.5, 2 * d, device=DEV)
+    plan = api.extend_plan(i32(cu), i32(kv), int(cu[-1]), H, Hkv, d, max(new), causal)
+    out = api.diffattn_extend(q, kc, vc, i32(table), plan, lam, 0.4, w)
+    _check_on_device(out, q, kc, vc, table, cu, kv, float(lam), w, causal)
+
+
+def test_extend_without_a_plan_of_its_sizes():
+    q, kc, vc, table, cu, plan, lam, w = _plain([1, 140], [50, 300], 2, 2, 64, 16)
+    out = torch.full((q.shape[0], 2, 128), 3.0, device=DEV).bfloat16()
+    for bad in (plan._replace(buf=torch.zeros_like(plan.buf)), plan._replace(buf=torch.full_like(plan.buf, 255)),
+                plan._replace(max_new=139)):
+        api.diffattn_extend(q, kc, vc, i32(table), bad, lam, 0.4, w, out=out)
+        assert api.device_status() == api.ERR_BOUNDS
+        assert (out == 3.0).all()
+
+
+def test_extend_of_no_rows_and_of_empty_requests():
+    lam, w = torch.tensor([0.3], device=DEV), torch.ones(128, device=DEV)
+    kc, vc = torch.zeros(2, 16, 2, 2, 64, device=DEV).bfloat16(), torch.zeros(2, 16, 2, 128, device=DEV).bfloat16()
+    bt = i32([[0], [1]])
+    for T, most in ((0, 0), (0, 5), (5, 5), (300, 300)):
+        plan = api.extend_plan(i32([0, 0, 0]), i32([3, 0]), T, 4, 2, 64, most)
+        out = torch.full((T, 4, 128), 3.0, device=DEV).bfloat16()
+        api.diffattn_extend(torch.zeros(T, 4, 2, 64, device=DEV).bfloat16(), kc, vc, bt, plan, lam, 0.4, w, out=out)
+        assert (out == 3.0).all()
+    assert api.device_status() == api.OK
+
+
+def test_extend_requests_on_the_same_pages():
+    """A shared prompt: two requests' tables name the same pages (each with its own last one)."""
+    q, kc, vc, table, cu, _, lam, w = _plain([1, 140], [50, 300], 2, 2, 64, 16)
+    shared = np.full((3, 19), -1)
+    shared[0], shared[1] = table[1], table[1]
+    shared[2, :3] = table[1, :3]
+    cu, kv = [0, 1, 140, 141], [300, 290, 48]
+    plan = api.extend_plan(i32(cu), i32(kv), q.shape[0], 2, 2, 64, 139)
+    out = api.diffattn_extend(q, kc, vc, i32(shared), plan, lam, 0.4, w)
+    _check(out, q, kc, vc, shared, cu, kv, float(lam), w)
+
+
 # ------------------------------------------------------------------ a run of them together --
 def _serve(schedule, x, H, Hkv, d, page, table, pages, T, check):
     """Two layers' caches served through the steps of `schedule` (new tokens per request); x: per layer (q, k, v) of
