@@ -33,6 +33,8 @@
 // finished here, or its unnormalised sums go to a record if the item is split.
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "extend.cuh"
 
@@ -49,8 +51,10 @@ template <int D>
 struct Narrow {
   static constexpr int DV = 2 * D;
   static constexpr int ROW = 4 * D;                     // bytes of a K or a V row
-  static constexpr int STAGE = kSlice * 2 * ROW;        // K rows, then V rows
-  static constexpr int STAGES = D == 128 ? 3 : 6;       // 48 KB a pair
+  static constexpr int SL = D == 128 ? 1 : 2;           // slices a step: 16 KB of keys and values
+  static constexpr int SLICE = kSlice * 2 * ROW;        // K rows, then V rows
+  static constexpr int STAGE = SL * SLICE;
+  static constexpr int STAGES = 3;                      // 48 KB a pair
   static constexpr int PITCH = DV + 4;                  // floats of a row of the merge buffer (no bank conflicts)
   static constexpr int OFF_BUF = kPairs * STAGES * STAGE;
   static constexpr int SMEM = OFF_BUF + kPairs * kNarrowRows * PITCH * 4;
@@ -115,9 +119,9 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) extend_narrow_kernel(const ExtendArgs a, float* recs, int page_shift,
                                                                     int max_keys, int one_unit, int* status) {
   using C = Narrow<D>;
-  constexpr int DV = C::DV, KS = D / 16, CT = DV / 16, R8 = kNarrowRows;
+  constexpr int DV = C::DV, KS = D / 16, CT = DV / 16, R8 = kNarrowRows, SL = C::SL;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float s_m[kPairs][2][R8], s_l[kPairs][2][R8], s_f[2][R8], s_ss[2 * kPairs][R8];
+  __shared__ float s_m[kPairs][2][R8], s_l[kPairs][2][R8], s_ss[2 * kPairs][R8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, pair = warp & (kPairs - 1), map = warp / kPairs;
   if (!plan_fits(a.plan, a.n, status)) return;
   const PlanView pv = plan_view(a.plan, a.n, 0);
@@ -136,28 +140,32 @@ __global__ void __launch_bounds__(kThreads, 1) extend_narrow_kernel(const Extend
   ld.hk = st.hk;
   ld.unit = st.unit;
   ld.open(pv.narrow);
-  const int slices = 2 * st.count;
+  constexpr int SPU = 2 / SL;  // steps a unit
+  const int steps = SPU * st.count;
   int issued = 0;
   auto issue = [&]() {
-    if (issued < slices) {
-      if (issued > 0 && !(issued & 1) && ++ld.unit == ld.units) ld.next(pv.narrow, H_kv);
+    if (issued < steps) {
+      if (issued > 0 && issued % SPU == 0 && ++ld.unit == ld.units) ld.next(pv.narrow, H_kv);
       const int L = min(ld.rq.L, max_keys);
-      const int key0 = ld.unit * kUnit + (issued & 1) * 64 + pair * kSlice;
-      if (key0 < L) {
-        const int page = a.block_table[static_cast<size_t>(ld.rq.s) * a.max_pages + (key0 >> page_shift)];
-        const bool ok = page >= 0 && page < a.num_pages;
-        if (!ok) atomicCAS(status, 0, 6);
-        constexpr int CH = C::ROW / 16, RPI = 32 / CH;  // 16-byte chunks of a row, rows an instruction
-        const int ch = lane % CH, r0 = lane / CH;
-        const size_t row0 = (static_cast<size_t>(ok ? page : 0) << page_shift) + (key0 & ((1 << page_shift) - 1));
-        const size_t pitch = static_cast<size_t>(H_kv) * C::ROW;
-        const char* src = cache + row0 * pitch + static_cast<size_t>(ld.hk) * C::ROW + 16 * ch;
-        const uint32_t dst = mine + (issued % C::STAGES) * C::STAGE;
-        const int rows = ok ? min(kSlice, L - key0) : 0;  // the rest is filled with zeros
 #pragma unroll
-        for (int i = 0; i < kSlice / RPI; ++i) {
-          const int r = i * RPI + r0;
-          cp16(dst + r * C::ROW + ((ch ^ (r & 7)) << 4), src + (r < rows ? r : 0) * pitch, r < rows ? 16 : 0);
+      for (int x = 0; x < SL; ++x) {
+        const int key0 = ld.unit * kUnit + (SL == 1 ? issued & 1 : x) * 64 + pair * kSlice;
+        if (key0 < L) {
+          const int page = a.block_table[static_cast<size_t>(ld.rq.s) * a.max_pages + (key0 >> page_shift)];
+          const bool ok = page >= 0 && page < a.num_pages;
+          if (!ok) atomicCAS(status, 0, 6);
+          constexpr int CH = C::ROW / 16, RPI = 32 / CH;  // 16-byte chunks of a row, rows an instruction
+          const int ch = lane % CH, r0 = lane / CH;
+          const size_t row0 = (static_cast<size_t>(ok ? page : 0) << page_shift) + (key0 & ((1 << page_shift) - 1));
+          const size_t pitch = static_cast<size_t>(H_kv) * C::ROW;
+          const char* src = cache + row0 * pitch + static_cast<size_t>(ld.hk) * C::ROW + 16 * ch;
+          const uint32_t dst = mine + (issued % C::STAGES) * C::STAGE + x * C::SLICE;
+          const int rows = ok ? min(kSlice, L - key0) : 0;  // the rest is filled with zeros
+#pragma unroll
+          for (int i = 0; i < kSlice / RPI; ++i) {
+            const int r = i * RPI + r0;
+            cp16(dst + r * C::ROW + ((ch ^ (r & 7)) << 4), src + (r < rows ? r : 0) * pitch, r < rows ? 16 : 0);
+          }
         }
       }
     }
@@ -175,7 +183,21 @@ __global__ void __launch_bounds__(kThreads, 1) extend_narrow_kernel(const Extend
   cur.hk = st.hk;
   cur.unit = st.unit;
   cur.open(pv.narrow);
-  int slice = 0;
+  // the queries of an item as the operand of S^T (this map's)
+  uint32_t qf[KS][2];
+  auto load_q = [&](const Cursor& it) {
+    const int R = it.rq.n * G, r = (lane >> 2) & (R <= R8 / 2 ? 3 : 7);
+    const uint32_t* qp =
+        static_cast<const uint32_t*>(a.q) +
+        ((static_cast<size_t>(it.rq.q0 + (r < R ? r / G : 0)) * H + it.hk * G + r % G) * DV + map * D) / 2 + (lane & 3);
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      qf[k][0] = r < R ? qp[8 * k] : 0u;
+      qf[k][1] = r < R ? qp[8 * k + 4] : 0u;
+    }
+  };
+  load_q(cur);
+  int step = 0;
   for (int left = st.count; left > 0;) {
     const int take = min(left, cur.units - cur.unit);
     const bool begins = cur.unit == 0, whole = begins && (take == cur.units || one_unit);
@@ -183,6 +205,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_narrow_kernel(const Extend
     const bool dup = R <= R8 / 2;  // columns 4 .. 7 hold rows 0 .. 3 again, with the remainders of their weights
     const int L = min(cur.rq.L, max_keys);
     if (cur.rq.L > max_keys && tid == 0) atomicCAS(status, 0, 6);
+    // the item behind this one: its request is read now and its queries before the merge, so that neither is waited for
+    Cursor nx = cur;
+    const bool more = left > take;
+    if (more) nx.next(pv.narrow, H_kv);
     // this thread's two columns of S^T and O^T and the last keys that their rows see
     int lim[2];
 #pragma unroll
@@ -192,111 +218,117 @@ __global__ void __launch_bounds__(kThreads, 1) extend_narrow_kernel(const Extend
     }
     const int lim_min = causal ? min(cur.rq.L - cur.rq.n, L - 1) : L - 1;
     const bool rest = dup && (lane & 2);  // this thread's columns are remainders
-    uint32_t qf[KS][2];
-    {
-      const int r = (lane >> 2) & (dup ? 3 : 7);
-      const uint32_t* qp =
-          static_cast<const uint32_t*>(a.q) +
-          ((static_cast<size_t>(cur.rq.q0 + (r < R ? r / G : 0)) * H + cur.hk * G + r % G) * DV + map * D) / 2 +
-          (lane & 3);
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        qf[k][0] = r < R ? qp[8 * k] : 0u;
-        qf[k][1] = r < R ? qp[8 * k + 4] : 0u;
-      }
-    }
     float o[CT][4], mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < CT; ++c)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[c][i] = 0.f;
-    for (int i = 0; i < 2 * take; ++i, ++slice) {
-      cp_wait<C::STAGES - 2>();
-      named_bar_sync(1 + pair, 64);  // both halves of the slice are here, and the slice before it has been read
-      issue();                       // into that one's stage
-      const int key0 = (cur.unit + (i >> 1)) * kUnit + (i & 1) * 64 + pair * kSlice;
-      if (key0 < L) {
-        const uint32_t kb = ring + (slice % C::STAGES) * C::STAGE, vb = kb + kSlice * C::ROW;
-        const int lr = lane & 7, mi = lane >> 3;
-        // S^T: keys x rows
-        float s[4];
-        {
-          const uint32_t base = kb + (lr + (mi & 1) * 8) * C::ROW;
-          float e[2][4] = {};  // two chains of products
+    // one loop for each way, so that neither carries the other's registers
+    auto steps_of = [&](auto dup_c) {
+      constexpr bool DUP = decltype(dup_c)::value;
+      for (int i = 0; i < SPU * take; ++i, ++step) {
+        cp_wait<C::STAGES - 2>();
+        named_bar_sync(1 + pair, 64);  // both halves of the step are here, and the step before it has been read
+        issue();                       // into that one's stage
+        const int unit0 = (cur.unit + i / SPU) * kUnit + pair * kSlice;
+        const int first = SL == 1 ? unit0 + (i & 1) * 64 : unit0;
+        if (first < L) {  // (a second slice without keys holds stale data: its scores are masked, and its V is not read)
+          const uint32_t kb = ring + (step % C::STAGES) * C::STAGE;
+          const int lr = lane & 7, mi = lane >> 3;
+          // S^T: keys x rows
+          float s[SL][4], t[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            uint32_t f[4];
-            ldsm4(f, base + (((map * (D / 8) + 2 * k + (mi >> 1)) ^ lr) << 4));
-            mma(e[k & 1], f, qf[k][0], qf[k][1]);
+          for (int x = 0; x < SL; ++x) {
+            const uint32_t base = kb + x * C::SLICE + (lr + (mi & 1) * 8) * C::ROW;
+            float e[2][4] = {};  // two chains of products
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              uint32_t f[4];
+              ldsm4(f, base + (((map * (D / 8) + 2 * k + (mi >> 1)) ^ lr) << 4));
+              mma(e[k & 1], f, qf[k][0], qf[k][1]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[x][j] = (e[0][j] + e[1][j]) * sc;
+            if (first + 64 * x + kSlice - 1 > lim_min) {
+              const int k_lo = first + 64 * x + (lane >> 2);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (k_lo + (j >> 1) * 8 > lim[j & 1]) s[x][j] = -INFINITY;
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) t[j] = fmaxf(t[j], fmaxf(s[x][j], s[x][j + 2]));
           }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s[j] = (e[0][j] + e[1][j]) * sc;
-        }
-        if (key0 + kSlice - 1 > lim_min) {
-          const int k_lo = key0 + (lane >> 2);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (k_lo + (j >> 1) * 8 > lim[j & 1]) s[j] = -INFINITY;
-        }
-        float t[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float x = fmaxf(s[j], s[j + 2]);
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          t[j] = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-        }
-        if (__any_sync(0xffffffffu, t[0] > mx[0] + kLazy || t[1] > mx[1] + kLazy)) {
-          float al[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float mn = fmaxf(mx[j], t[j]);
-            al[j] = mn == -INFINITY ? 1.f : fast_exp2(mx[j] - mn);
-            mx[j] = mn;
-            l[j] *= al[j];
+            t[j] = fmaxf(t[j], __shfl_xor_sync(0xffffffffu, t[j], 4));
+            t[j] = fmaxf(t[j], __shfl_xor_sync(0xffffffffu, t[j], 8));
+            t[j] = fmaxf(t[j], __shfl_xor_sync(0xffffffffu, t[j], 16));
+          }
+          if (__any_sync(0xffffffffu, t[0] > mx[0] + kLazy || t[1] > mx[1] + kLazy)) {
+            float al[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float mn = fmaxf(mx[j], t[j]);
+              al[j] = mn == -INFINITY ? 1.f : fast_exp2(mx[j] - mn);
+              mx[j] = mn;
+              l[j] *= al[j];
+            }
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[c][j] *= al[j & 1];
+            }
           }
 #pragma unroll
-          for (int c = 0; c < CT; ++c) {
+          for (int x = 0; x < SL; ++x) {
+            if (x > 0 && first + 64 * x >= L) break;
+            uint32_t pb[2], pl[2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[c][j] *= al[j & 1];
-          }
-        }
-        uint32_t pb[2], pl[2];
+            for (int j = 0; j < 2; ++j) {
+              const float p0 = fast_exp2(s[x][2 * j] - (mx[0] == -INFINITY ? 0.f : mx[0]));
+              const float p1 = fast_exp2(s[x][2 * j + 1] - (mx[1] == -INFINITY ? 0.f : mx[1]));
+              l[0] += p0;
+              l[1] += p1;
+              const uint32_t hi = pack_bf16x2(p0, p1);
+              const uint32_t lo = pack_bf16x2(p0 - bf16lo_to_f32(hi), p1 - bf16hi_to_f32(hi));
+              pb[j] = transpose8x8(DUP && rest ? lo : hi);
+              pl[j] = lo;
+            }
+            // O^T += V^T P^T: channels x rows
+            const uint32_t base = kb + x * C::SLICE + (kSlice + lr + (mi >> 1) * 8) * C::ROW;
+            if constexpr (DUP) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float p0 = fast_exp2(s[2 * j] - (mx[0] == -INFINITY ? 0.f : mx[0]));
-          const float p1 = fast_exp2(s[2 * j + 1] - (mx[1] == -INFINITY ? 0.f : mx[1]));
-          l[0] += p0;
-          l[1] += p1;
-          const uint32_t hi = pack_bf16x2(p0, p1);
-          const uint32_t lo = pack_bf16x2(p0 - bf16lo_to_f32(hi), p1 - bf16hi_to_f32(hi));
-          pb[j] = transpose8x8(rest ? lo : hi);
-          pl[j] = lo;
-        }
-        // O^T += V^T P^T: channels x rows
-        const uint32_t base = vb + (lr + (mi >> 1) * 8) * C::ROW;
-        if (dup) {
+              for (int c = 0; c < CT; ++c) {
+                uint32_t f[4];
+                ldsm4t(f, base + (((2 * c + (mi & 1)) ^ lr) << 4));
+                mma(o[c], f, pb[0], pb[1]);
+              }
+            } else {
+              pl[0] = transpose8x8(pl[0]);
+              pl[1] = transpose8x8(pl[1]);
 #pragma unroll
-          for (int c = 0; c < CT; ++c) {
-            uint32_t f[4];
-            ldsm4t(f, base + (((2 * c + (mi & 1)) ^ lr) << 4));
-            mma(o[c], f, pb[0], pb[1]);
-          }
-        } else {
-          pl[0] = transpose8x8(pl[0]);
-          pl[1] = transpose8x8(pl[1]);
-#pragma unroll
-          for (int c = 0; c < CT; ++c) {
-            uint32_t f[4];
-            ldsm4t(f, base + (((2 * c + (mi & 1)) ^ lr) << 4));
-            mma(o[c], f, pb[0], pb[1]);
-            mma(o[c], f, pl[0], pl[1]);
+              for (int c = 0; c < CT; ++c) {
+                uint32_t f[4];
+                ldsm4t(f, base + (((2 * c + (mi & 1)) ^ lr) << 4));
+                mma(o[c], f, pb[0], pb[1]);
+                mma(o[c], f, pl[0], pl[1]);
+              }
+            }
           }
         }
       }
-    }
+    };
+    if (dup)
+      steps_of(std::true_type{});
+    else
+      steps_of(std::false_type{});
+    if (more) load_q(nx);
 
     // ------------------------------------------------- merge of the pairs --
+    // Every warp leaves its maxima, sums and unnormalised O^T; the thread that
+    // finishes a channel takes the four pairs' to their common maximum itself.
+    // With up to four rows both maps fit the buffer (rows 0 .. 3 and 4 .. 7)
+    // and one barrier does; with more the maps go through it one by one.
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       float x = l[j];
@@ -308,61 +340,59 @@ __global__ void __launch_bounds__(kThreads, 1) extend_narrow_kernel(const Extend
         s_m[pair][map][2 * lane + j] = mx[j];
       }
     }
-    __syncthreads();
+    if (dup) {  // the weights' and their remainders' products
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[c][j] += __shfl_xor_sync(0xffffffffu, o[c][j], 2);
+    }
     // The item's record, for a part of it that the joining kernel reads.
     float* rec = recs + (2 * blockIdx.x + (begins ? 1 : 0)) * record_floats(R8, D);
     const bool part = !whole && !(one_unit && !begins);
-    if (tid < 2 * R8) {
-      const int m = tid / R8, r = tid % R8;
-      float M = -INFINITY, sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < kPairs; ++w) M = fmaxf(M, s_m[w][m][r]);
-#pragma unroll
-      for (int w = 0; w < kPairs; ++w)
-        sum = fmaf(M == -INFINITY ? 0.f : fast_exp2(s_m[w][m][r] - M), s_l[w][m][r], sum);
-      s_f[m][r] = sum > 0.f ? (m ? c2 : 1.f) / sum : 0.f;
-      if (part && r < R) {
-        rec[4 * r + 2 * m] = M;
-        rec[4 * r + 2 * m + 1] = sum;
-      }
-    }
-    float f[2];  // this warp's sums to the common maximum
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int c = 2 * (lane & 3) + j;
-      float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kPairs; ++w) M = fmaxf(M, s_m[w][map][c]);
-      f[j] = M == -INFINITY ? 0.f : fast_exp2(mx[j] - M);
-    }
     // a thread finishes channel ch of every NG-th row
     constexpr int NG = kThreads / DV, NR = R8 / NG;
     const int ch = tid % DV, rg = tid / DV;
     float y[NR];
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      if (m) __syncthreads();  // the buffer's first map has been read
-      if (map == m) {
-        float* to = buf + static_cast<size_t>(pair) * R8 * C::PITCH;
+    for (int k = 0; k < NR; ++k) y[k] = 0.f;
+    for (int phase = 0; phase < (dup ? 1 : 2); ++phase) {
+      if (phase) __syncthreads();  // the buffer's first map has been read
+      if (dup || map == phase) {
+        float* to = buf + static_cast<size_t>(pair * R8 + (dup ? 4 * map : 0)) * C::PITCH + (lane >> 2);
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
+        for (int j = 0; j < 2; ++j) {
+          const int r = 2 * (lane & 3) + j;
+          if (r < R) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int r = 2 * (lane & 3) + (j & 1);
-            if ((r & (dup ? 3 : 7)) < R) to[r * C::PITCH + 16 * c + (lane >> 2) + (j >> 1) * 8] = o[c][j] * f[j & 1];
+            for (int c = 0; c < CT; ++c) {
+              to[r * C::PITCH + 16 * c] = o[c][j];
+              to[r * C::PITCH + 16 * c + 8] = o[c][j + 2];
+            }
           }
+        }
       }
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < NR; ++k) {
         const int r = rg + k * NG;
         if (r < R) {
-          const float* b = buf + r * C::PITCH + ch;
-          float x = 0.f;
+          for (int m = dup ? 0 : phase; m < (dup ? 2 : phase + 1); ++m) {
+            float M = -INFINITY, sum = 0.f, x = 0.f;
 #pragma unroll
-          for (int w = 0; w < kPairs; ++w) x += b[w * R8 * C::PITCH] + (dup ? b[(w * R8 + 4) * C::PITCH] : 0.f);
-          if (part) rec[4 * R8 + static_cast<size_t>(r) * 2 * DV + m * DV + ch] = x;
-          y[k] = m ? fmaf(x, s_f[1][r], y[k]) : x * s_f[0][r];
+            for (int w = 0; w < kPairs; ++w) M = fmaxf(M, s_m[w][m][r]);
+            const float* b = buf + (dup ? 4 * m + r : r) * C::PITCH + ch;
+#pragma unroll
+            for (int w = 0; w < kPairs; ++w) {
+              const float f = M == -INFINITY ? 0.f : fast_exp2(s_m[w][m][r] - M);
+              sum = fmaf(f, s_l[w][m][r], sum);
+              x = fmaf(f, b[w * R8 * C::PITCH], x);
+            }
+            if (part) {
+              rec[4 * R8 + static_cast<size_t>(r) * 2 * DV + m * DV + ch] = x;
+              if (ch == 0) *reinterpret_cast<float2*>(rec + 4 * r + 2 * m) = make_float2(M, sum);
+            }
+            y[k] = fmaf(x, sum > 0.f ? (m ? c2 : 1.f) / sum : 0.f, y[k]);
+          }
         }
       }
     }
@@ -377,7 +407,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_narrow_kernel(const Extend
           if (lane == 0) s_ss[warp][r] = ss;
         }
       }
-      __syncthreads();
+    }
+    // the merge's buffers are free for the next item (its sums of squares come behind its own barrier)
+    __syncthreads();
+    if (whole) {
 #pragma unroll
       for (int k = 0; k < NR; ++k) {
         const int r = rg + k * NG;
@@ -391,9 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_narrow_kernel(const Extend
         }
       }
     }
-    __syncthreads();  // the merge's shared memory is free again
     left -= take;
-    if (left > 0) cur.next(pv.narrow, H_kv);
+    cur = nx;
   }
   cp_wait<0>();
 }
