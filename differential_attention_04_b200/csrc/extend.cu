@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
 // maximum and added in the order of the keys (many parts: within eight groups,
 // then group by group), then comes the epilogue of a whole row.  Reads 16 d
 // bytes a part and row; with one block a row for every worker it took 48 us
-// where this takes JOIN_US (a mixed step of 20 over 4 heads, d 128).
+// where this takes 15 (a mixed step of 20 over 4 heads, d 128).
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinFew = kJoinWarps;  // parts up to which a warp takes a row alone
@@ -401,11 +401,20 @@ __global__ void __launch_bounds__(kJoinThreads) extend_join_kernel(const ExtendA
   __shared__ float2 f[kNarrowWorkers];  // factors of a part's two maps
   __shared__ float red[4][kJoinWarps];
   __shared__ float acc[kJoinWarps][2 * DV];
-  static_assert(kNarrowWorkers <= kJoinThreads, "one thread per part");
+  constexpr int PT = (kNarrowWorkers + kJoinThreads - 1) / kJoinThreads;  // parts of a thread
   for (int r = team; r < R; r += teams) {
-    float4 ml = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-    if (tid < tl.parts) ml = *reinterpret_cast<const float4*>(part(tid) + 4 * r);
-    float M1 = max_of(ml.x), M2 = max_of(ml.z);
+    float4 ml[PT];
+    float M1 = -INFINITY, M2 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+      const int p = tid + i * kJoinThreads;
+      ml[i] = p < tl.parts ? *reinterpret_cast<const float4*>(part(p) + 4 * r)
+                           : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+      M1 = fmaxf(M1, ml[i].x);
+      M2 = fmaxf(M2, ml[i].z);
+    }
+    M1 = max_of(M1);
+    M2 = max_of(M2);
     if (lane == 0) {
       red[0][warp] = M1;
       red[1][warp] = M2;
@@ -416,9 +425,18 @@ __global__ void __launch_bounds__(kJoinThreads) extend_join_kernel(const ExtendA
       M1 = fmaxf(M1, red[0][g]);
       M2 = fmaxf(M2, red[1][g]);
     }
-    const float f1 = M1 == -INFINITY ? 0.f : fast_exp2(ml.x - M1), f2 = M2 == -INFINITY ? 0.f : fast_exp2(ml.z - M2);
-    if (tid < tl.parts) f[tid] = make_float2(f1, f2);
-    float l1 = sum_of(f1 * ml.y), l2 = sum_of(f2 * ml.w);
+    float l1 = 0.f, l2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+      const int p = tid + i * kJoinThreads;
+      const float f1 = M1 == -INFINITY ? 0.f : fast_exp2(ml[i].x - M1);
+      const float f2 = M2 == -INFINITY ? 0.f : fast_exp2(ml[i].z - M2);
+      if (p < tl.parts) f[p] = make_float2(f1, f2);
+      l1 = fmaf(f1, ml[i].y, l1);
+      l2 = fmaf(f2, ml[i].w, l2);
+    }
+    l1 = sum_of(l1);
+    l2 = sum_of(l2);
     if (lane == 0) {
       red[2][warp] = l1;
       red[3][warp] = l2;

@@ -37,7 +37,7 @@ constexpr int kWideRows = 128;
 // with 7).  A narrow item's end is hidden by the loads that run ahead.
 constexpr int kNarrowCost = 0;
 __host__ __device__ constexpr int wide_cost(int d) { return d == 64 ? 3 : 7; }
-constexpr int kNarrowWorkers = 148;  // one CTA per SM
+constexpr int kNarrowWorkers = 296;  // two CTAs per SM
 // One CTA per SM (both maps), or one CTA pair per two SMs (a map each): two
 // output tiles of 2 d = 128 columns fit tensor memory, two of 256 do not.
 __host__ __device__ constexpr int wide_workers(int d) { return d == 64 ? 148 : 74; }

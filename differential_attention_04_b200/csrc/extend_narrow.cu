@@ -15,22 +15,30 @@
 // remainders take the four free columns, at no cost; with five to eight they
 // are a second product into the same sums.
 //
-// A CTA of four pairs of warps per SM takes a contiguous range of the step's
-// units of 128 keys (extend.cuh).  Within a unit pair w takes keys 16 w ..
-// 16 w + 15 and the same 64 on; a slice of 16 keys lies in one page.  One warp
-// of a pair computes map 1 and loads the keys, the other map 2 and the values:
-// two warps per scheduler hide each other's latencies (one warp with both
-// maps: 1943 us against TWO_WARPS for 64 requests of 1K to 32K tokens, 12 heads,
-// d 128).  A pair streams its slices through its own ring of stages with
-// 16-byte cp.async (one page lookup a slice; rows behind the cached ones are
-// filled with zeros, so what the page holds there never enters) and meets at
-// one barrier a slice; pairs do not wait for each other.  128 KB are in flight
-// per SM, and the loads run ahead across the borders of items.  Per slice:
-// scores, online softmax in the log2 domain with a lazy rescale (only when the
-// maximum has grown by more than 2^8), V^T P^T.  S^T's accumulators become
-// P^T's operand by one 8x8 transposition in registers (movmatrix).  At the end
-// of an item the pairs' states are merged through shared memory and the row is
-// finished here, or its unnormalised sums go to a record if the item is split.
+// Two CTAs of two pairs of warps per SM take a contiguous range of the step's
+// units of 128 keys each (extend.cuh).  Within a unit the pairs take turns of
+// 16 keys; a slice of 16 keys lies in one page.  One warp of a pair computes
+// map 1 and loads the keys, the other map 2 and the values: two warps per
+// scheduler hide each other's latencies (one warp with both maps and the
+// product for the remainders: 2272 us for 64 requests of 1K to 32K tokens, 12
+// heads, d 128; two warps: 1845).  A pair streams its slices through its own
+// ring of stages with 16-byte cp.async (one page lookup a slice; rows behind
+// the cached ones are filled with zeros, so what the page holds there never
+// enters) and meets at one barrier a step; pairs do not wait for each other.
+// 128 KB are in flight per SM, and the loads run ahead across the borders of
+// items.  Per step: scores, online softmax in the log2 domain with a lazy
+// rescale (only when the maximum has grown by more than 2^8), V^T P^T.  S^T's
+// accumulators become P^T's operand by one 8x8 transposition in registers
+// (movmatrix).  At the end of an item the pairs' states are merged through
+// shared memory and the row is finished here, or its unnormalised sums go to a
+// record if the item is split.  The second CTA of an SM loads and computes
+// under the first one's merge: one CTA of four pairs took 141 us for 256
+// requests of 80 tokens over 16 heads where this takes 88, and 386 us for 24 x 5
+// drafted tokens where this takes 355 (a lone request of 1000 tokens: 14 and 17
+// us).
+//
+// Measured (d 128): the 64 requests above 1764 us, 7.2 TB/s of keys and values;
+// the drafted tokens 355 us, 6.0 TB/s.
 #include <math.h>
 
 #include <type_traits>
@@ -42,7 +50,7 @@ namespace diffattn {
 
 namespace {
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kPairs = 4;
+constexpr int kPairs = 2;
 constexpr int kThreads = 2 * kPairs * 32;
 constexpr int kSlice = 16;
 constexpr float kLazy = 8.0f;  // log2 units
@@ -58,7 +66,7 @@ struct Narrow {
   static constexpr int PITCH = DV + 4;                  // floats of a row of the merge buffer (no bank conflicts)
   static constexpr int OFF_BUF = kPairs * STAGES * STAGE;
   static constexpr int SMEM = OFF_BUF + kPairs * kNarrowRows * PITCH * 4;
-  static_assert(SMEM + 1024 <= 232448, "shared memory per CTA");
+  static_assert(2 * (SMEM + 1024 + 512) <= 233472, "shared memory of two CTAs");
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -116,7 +124,7 @@ struct Cursor {
 // one_unit: the block table holds at most kUnit keys, so a unit behind an
 // item's first has none, and the first is the whole item.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) extend_narrow_kernel(const ExtendArgs a, float* recs, int page_shift,
+__global__ void __launch_bounds__(kThreads, 2) extend_narrow_kernel(const ExtendArgs a, float* recs, int page_shift,
                                                                     int max_keys, int one_unit, int* status) {
   using C = Narrow<D>;
   constexpr int DV = C::DV, KS = D / 16, CT = DV / 16, R8 = kNarrowRows, SL = C::SL;
@@ -140,7 +148,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_narrow_kernel(const Extend
   ld.hk = st.hk;
   ld.unit = st.unit;
   ld.open(pv.narrow);
-  constexpr int SPU = 2 / SL;  // steps a unit
+  constexpr int SPU = kUnit / (kPairs * kSlice * SL);  // steps a unit
+  // where step i's slice x of this pair begins in the unit
+  auto slice_at = [&](int i, int x) { return ((i % SPU * SL + x) * kPairs + pair) * kSlice; };
   const int steps = SPU * st.count;
   int issued = 0;
   auto issue = [&]() {
@@ -149,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_narrow_kernel(const Extend
       const int L = min(ld.rq.L, max_keys);
 #pragma unroll
       for (int x = 0; x < SL; ++x) {
-        const int key0 = ld.unit * kUnit + (SL == 1 ? issued & 1 : x) * 64 + pair * kSlice;
+        const int key0 = ld.unit * kUnit + slice_at(issued, x);
         if (key0 < L) {
           const int page = a.block_table[static_cast<size_t>(ld.rq.s) * a.max_pages + (key0 >> page_shift)];
           const bool ok = page >= 0 && page < a.num_pages;
@@ -230,8 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_narrow_kernel(const Extend
         cp_wait<C::STAGES - 2>();
         named_bar_sync(1 + pair, 64);  // both halves of the step are here, and the step before it has been read
         issue();                       // into that one's stage
-        const int unit0 = (cur.unit + i / SPU) * kUnit + pair * kSlice;
-        const int first = SL == 1 ? unit0 + (i & 1) * 64 : unit0;
+        const int first = (cur.unit + i / SPU) * kUnit + slice_at(i, 0);
         if (first < L) {  // (a second slice without keys holds stale data: its scores are masked, and its V is not read)
           const uint32_t kb = ring + (step % C::STAGES) * C::STAGE;
           const int lr = lane & 7, mi = lane >> 3;
@@ -249,8 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_narrow_kernel(const Extend
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[x][j] = (e[0][j] + e[1][j]) * sc;
-            if (first + 64 * x + kSlice - 1 > lim_min) {
-              const int k_lo = first + 64 * x + (lane >> 2);
+            if (first + kPairs * kSlice * x + kSlice - 1 > lim_min) {
+              const int k_lo = first + kPairs * kSlice * x + (lane >> 2);
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 if (k_lo + (j >> 1) * 8 > lim[j & 1]) s[x][j] = -INFINITY;
@@ -281,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_narrow_kernel(const Extend
           }
 #pragma unroll
           for (int x = 0; x < SL; ++x) {
-            if (x > 0 && first + 64 * x >= L) break;
+            if (x > 0 && first + kPairs * kSlice * x >= L) break;
             uint32_t pb[2], pl[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -349,12 +358,13 @@ __global__ void __launch_bounds__(kThreads, 1) extend_narrow_kernel(const Extend
     // The item's record, for a part of it that the joining kernel reads.
     float* rec = recs + (2 * blockIdx.x + (begins ? 1 : 0)) * record_floats(R8, D);
     const bool part = !whole && !(one_unit && !begins);
-    // a thread finishes channel ch of every NG-th row
-    constexpr int NG = kThreads / DV, NR = R8 / NG;
-    const int ch = tid % DV, rg = tid / DV;
-    float y[NR];
+    // a thread finishes channels tid, tid + kThreads, ... of every row
+    constexpr int E = DV / kThreads;
+    float y[R8][E];
 #pragma unroll
-    for (int k = 0; k < NR; ++k) y[k] = 0.f;
+    for (int r = 0; r < R8; ++r)
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[r][e] = 0.f;
     for (int phase = 0; phase < (dup ? 1 : 2); ++phase) {
       if (phase) __syncthreads();  // the buffer's first map has been read
       if (dup || map == phase) {
@@ -373,35 +383,39 @@ __global__ void __launch_bounds__(kThreads, 1) extend_narrow_kernel(const Extend
       }
       __syncthreads();
 #pragma unroll
-      for (int k = 0; k < NR; ++k) {
-        const int r = rg + k * NG;
+      for (int r = 0; r < R8; ++r) {
         if (r < R) {
           for (int m = dup ? 0 : phase; m < (dup ? 2 : phase + 1); ++m) {
-            float M = -INFINITY, sum = 0.f, x = 0.f;
+            float M = -INFINITY, sum = 0.f, f[kPairs];
 #pragma unroll
             for (int w = 0; w < kPairs; ++w) M = fmaxf(M, s_m[w][m][r]);
-            const float* b = buf + (dup ? 4 * m + r : r) * C::PITCH + ch;
 #pragma unroll
             for (int w = 0; w < kPairs; ++w) {
-              const float f = M == -INFINITY ? 0.f : fast_exp2(s_m[w][m][r] - M);
-              sum = fmaf(f, s_l[w][m][r], sum);
-              x = fmaf(f, b[w * R8 * C::PITCH], x);
+              f[w] = M == -INFINITY ? 0.f : fast_exp2(s_m[w][m][r] - M);
+              sum = fmaf(f[w], s_l[w][m][r], sum);
             }
-            if (part) {
-              rec[4 * R8 + static_cast<size_t>(r) * 2 * DV + m * DV + ch] = x;
-              if (ch == 0) *reinterpret_cast<float2*>(rec + 4 * r + 2 * m) = make_float2(M, sum);
+            const float scale = sum > 0.f ? (m ? c2 : 1.f) / sum : 0.f;
+            if (part && tid == 0) *reinterpret_cast<float2*>(rec + 4 * r + 2 * m) = make_float2(M, sum);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              const float* b = buf + (dup ? 4 * m + r : r) * C::PITCH + tid + e * kThreads;
+              float x = 0.f;
+#pragma unroll
+              for (int w = 0; w < kPairs; ++w) x = fmaf(f[w], b[w * R8 * C::PITCH], x);
+              if (part) rec[4 * R8 + static_cast<size_t>(r) * 2 * DV + m * DV + tid + e * kThreads] = x;
+              y[r][e] = fmaf(x, scale, y[r][e]);
             }
-            y[k] = fmaf(x, sum > 0.f ? (m ? c2 : 1.f) / sum : 0.f, y[k]);
           }
         }
       }
     }
     if (whole) {  // the same for the whole CTA
 #pragma unroll
-      for (int k = 0; k < NR; ++k) {
-        const int r = rg + k * NG;
-        if (r < R) {  // the same for a whole warp
-          float ss = y[k] * y[k];
+      for (int r = 0; r < R8; ++r) {
+        if (r < R) {
+          float ss = 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) ss = fmaf(y[r][e], y[r][e], ss);
 #pragma unroll
           for (int off = 16; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
           if (lane == 0) s_ss[warp][r] = ss;
@@ -412,15 +426,19 @@ __global__ void __launch_bounds__(kThreads, 1) extend_narrow_kernel(const Extend
     __syncthreads();
     if (whole) {
 #pragma unroll
-      for (int k = 0; k < NR; ++k) {
-        const int r = rg + k * NG;
+      for (int r = 0; r < R8; ++r) {
         if (r < R) {
           float ss = 0.f;
 #pragma unroll
-          for (int w = 0; w < DV / 32; ++w) ss += s_ss[rg * (DV / 32) + w][r];
+          for (int w = 0; w < 2 * kPairs; ++w) ss += s_ss[w][r];
           const float gsc = (1.f - a.lambda_init) * rsqrtf(ss / DV + a.eps);
           const size_t row = static_cast<size_t>(cur.rq.q0 + r / G) * H + cur.hk * G + r % G;
-          static_cast<__nv_bfloat16*>(a.o)[row * DV + ch] = __float2bfloat16_rn(y[k] * gsc * __ldg(a.rms_w + ch));
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const int ch = tid + e * kThreads;
+            static_cast<__nv_bfloat16*>(a.o)[row * DV + ch] =
+                __float2bfloat16_rn(y[r][e] * gsc * __ldg(a.rms_w + ch));
+          }
         }
       }
     }

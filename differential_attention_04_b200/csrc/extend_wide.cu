@@ -30,8 +30,14 @@
 // barriers are the prefill's; barrier phases count segments (epi_free), tiles
 // (K, V, S, P) or combined segments (the exchange).
 //
-// Bound: the tensor cores for long chunks (12 d flops per query, key and head);
-// memory for few rows over many keys.
+// Bound: as the prefill, the softmax warps and the serial issue of products
+// (about 2500 cycles a 128-key tile against 1540 of tensor work) for long
+// chunks; memory for few rows over many keys; and about 20 thousand cycles an
+// item for its exchange and refill, which short prompts feel (74 x 128 tokens
+// over 12 heads: 147 us).  Measured: 2048 tokens behind 30K cached ones over 12
+// heads 906 us at full clock (1290 TFLOP/s), 1083 us in a loop under the power
+// cap; 2048 behind 6K 244 us.  Two softmax warpgroups with 64 keys each were
+// not faster here (chunk 1285 against 1280 us, mixed step 136 against 132).
 #include "extend_wide.cuh"
 
 namespace diffattn {
