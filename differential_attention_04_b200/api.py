@@ -497,7 +497,8 @@ def paged_step(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torc
     _i32("ctx_lens", ctx_lens, S)
     _i32("new_lens", new_lens, S)
     _i32("block_table", block_table, S, max_pages)
-    _i32("free_pages", free_pages, free_pages.numel())
+    F = free_pages.numel()
+    _i32("free_pages", free_pages, F)
     _i32("pool", pool, 2)
     if pool_out is None:
         pool_out = pool
@@ -513,9 +514,9 @@ def paged_step(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torc
         ts += tuple(out)
     cu_q, kv_lens, positions, slots, info = out
     _launch("diffattn_paged_step", ts,
-            _ptr(ctx_lens), _ptr(new_lens), S, _ptr(block_table), max_pages, _ptr(free_pages), free_pages.numel(),
-            _ptr(pool), _ptr(pool_out), int(page_size), T, _ptr(cu_q), _ptr(kv_lens), _ptr(positions), _ptr(slots),
-            _ptr(info))
+            ctx_lens.data_ptr(), new_lens.data_ptr(), S, block_table.data_ptr(), max_pages, free_pages.data_ptr(), F,
+            pool.data_ptr(), pool_out.data_ptr(), int(page_size), T, cu_q.data_ptr(), kv_lens.data_ptr(),
+            positions.data_ptr(), slots.data_ptr(), info.data_ptr())
     return cu_q, kv_lens, positions, slots, info
 
 
@@ -530,11 +531,13 @@ def rope_table_scaled(N: int, rot: int, base: float = 10000.0, scaling: int = RO
     return t
 
 
-def _rope_args(q, positions, table, T):
-    _need(table.dtype == torch.float32 and table.dim() == 3 and table.shape[2] == 2 and table.shape[0] >= 1 and
-          2 <= 2 * table.shape[1] <= q.shape[-1], "table must be float32 [n_pos, rot/2, 2] with rot <= d")
-    _need(positions.dtype == torch.int32 and positions.numel() == T, "positions must be int32 with one entry per row")
-    return table.shape[0], 2 * table.shape[1]
+def _rope_args(d, positions, table, T):
+    ts = table.shape
+    if table.dtype is not torch.float32 or len(ts) != 3 or ts[2] != 2 or ts[0] < 1 or not 1 <= ts[1] <= d // 2:
+        raise ValueError("table must be float32 [n_pos, rot/2, 2] with rot <= d")
+    if positions.dtype is not torch.int32 or positions.numel() != T:
+        raise ValueError("positions must be int32 with one entry per row")
+    return ts[0], 2 * ts[1]
 
 
 def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table: torch.Tensor,
@@ -544,40 +547,51 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table
     rope_table_scaled, whose width says how many channels are rotated.  Rows with a negative position are left as
     they are in `out` (which may be (q, k) itself).  ``inverse`` is the transposed map: gradients with respect to
     q', k' go in, those with respect to q, k come out."""
-    _need(q.dim() >= 4 and q.shape[-2] == 2, "q must be [..., H, 2, d]")
-    H, d = q.shape[-3], q.shape[-1]
+    qs = q.shape
+    _need(len(qs) >= 4 and qs[-2] == 2, "q must be [..., H, 2, d]")
+    H, d = qs[-3], qs[-1]
     T = positions.numel()
     _need(q.numel() == T * H * 2 * d, "positions must be int32 with one entry per row")
     dt = BF16 if q.dtype == torch.bfloat16 else F32 if q.dtype == torch.float32 else None
     _need(dt is not None, "dtype must be bfloat16 or float32")
     H_kv = 0
     if k is not None:
-        _need(k.dim() == q.dim() and k.shape[:-3] == q.shape[:-3] and tuple(k.shape[-2:]) == (2, d) and
-              k.dtype == q.dtype, "k must be [..., H_kv, 2, d] with q's rows and dtype")
-        H_kv = k.shape[-3]
-    n_pos, rot = _rope_args(q, positions, table, T)
+        ks = k.shape
+        _need(len(ks) == len(qs) and ks[:-3] == qs[:-3] and ks[-2:] == (2, d) and k.dtype is q.dtype,
+              "k must be [..., H_kv, 2, d] with q's rows and dtype")
+        H_kv = ks[-3]
+    n_pos, rot = _rope_args(d, positions, table, T)
     if out is None:
         out = (torch.empty_like(q), None if k is None else torch.empty_like(k))
     _need(len(out) == 2, "out must hold (q', k')")
     qo, ko = out
-    _same("q'", qo, q.shape, q.dtype)
+    _same("q'", qo, qs, q.dtype)
     _need((ko is None) == (k is None), "out must hold k' exactly when k is given")
     ts = (q, positions, table, qo)
     if k is not None:
-        _same("k'", ko, k.shape, k.dtype)
+        _same("k'", ko, ks, k.dtype)
         ts += (k, ko)
-    _launch("diffattn_rope", ts, _ptr(q), _ptr(k), _ptr(positions), _ptr(table), n_pos, T, H, H_kv, d, rot, dt,
-            int(layout), int(bool(inverse)), _ptr(qo), _ptr(ko))
+    _launch("diffattn_rope", ts, q.data_ptr(), _ptr(k), positions.data_ptr(), table.data_ptr(), n_pos, T, H, H_kv, d,
+            rot, dt, int(layout), int(bool(inverse)), qo.data_ptr(), _ptr(ko))
     return qo, ko
 
 
 def _cache_shapes(k_cache, v_cache, d, dtype):
     """(num_pages, page_size, H_kv) of a paged cache."""
-    _need(k_cache.dim() == 5 and tuple(k_cache.shape[3:]) == (2, d) and k_cache.dtype == dtype,
-          "k_cache must be [num_pages, page_size, H_kv, 2, d] of q's dtype")
-    P, ps, H_kv = k_cache.shape[:3]
+    s = k_cache.shape
+    if len(s) != 5 or s[3] != 2 or s[4] != d or k_cache.dtype is not dtype:
+        raise ValueError("k_cache must be [num_pages, page_size, H_kv, 2, d] of q's dtype")
+    P, ps, H_kv, _, _ = s
     _same("v_cache", v_cache, (P, ps, H_kv, 2 * d), dtype)
     return P, ps, H_kv
+
+
+def _rows(q):
+    """(T, H, d) of a step's queries."""
+    s = q.shape
+    if len(s) != 4 or s[2] != 2 or q.dtype is not torch.bfloat16:
+        raise ValueError("q must be bfloat16 [T, H, 2, d]")
+    return s[0], s[1], s[3]
 
 
 def kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor | None, slots: torch.Tensor,
@@ -586,24 +600,23 @@ def kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torc
     """The cache write of a step: returns q rotated at `positions`, and writes k rotated and v into the pages at
     `slots` (int32 [T], page * page_size + offset; negative: nothing is written).  q: bfloat16 [T, H, 2, d];
     k: [T, H_kv, 2, d]; v: [T, H_kv, 2d]; table None: no rotation."""
-    _need(q.dim() == 4 and q.shape[2] == 2 and q.dtype == torch.bfloat16, "q must be bfloat16 [T, H, 2, d]")
-    T, H, _, d = q.shape
+    T, H, d = _rows(q)
     num_pages, page_size, H_kv = _cache_shapes(k_cache, v_cache, d, torch.bfloat16)
     _same("k", k, (T, H_kv, 2, d), torch.bfloat16)
     _same("v", v, (T, H_kv, 2 * d), torch.bfloat16)
     _i32("slots", slots, T)
     n_pos = rot = 0
-    ts = (q, k, v, slots, k_cache, v_cache)
-    if table is not None:
-        _need(positions is not None, "positions must be int32 with one entry per row")
-        n_pos, rot = _rope_args(q, positions, table, T)
-        ts += (positions, table)
     if out is None:
         out = torch.empty_like(q)
-    _same("out", out, q.shape, q.dtype)
-    _launch("diffattn_kv_append", ts + (out,), _ptr(q), _ptr(k), _ptr(v),
-            None if table is None else _ptr(positions), _ptr(slots), _ptr(table), n_pos, T, H, H_kv, d, rot,
-            int(layout), num_pages, page_size, _ptr(out), _ptr(k_cache), _ptr(v_cache))
+    _same("out", out, (T, H, 2, d), torch.bfloat16)
+    ts = (q, k, v, slots, k_cache, v_cache, out)
+    if table is not None:
+        _need(positions is not None, "positions must be int32 with one entry per row")
+        n_pos, rot = _rope_args(d, positions, table, T)
+        ts += (positions, table)
+    _launch("diffattn_kv_append", ts, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            None if table is None else positions.data_ptr(), slots.data_ptr(), _ptr(table), n_pos, T, H, H_kv, d, rot,
+            int(layout), num_pages, page_size, out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr())
     return out
 
 
@@ -645,12 +658,12 @@ def diffattn_extend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     """Differential attention of the step's new tokens over the paged cache.  q: bfloat16 [T, H, 2, d]; k_cache:
     [num_pages, page_size, H_kv, 2, d]; v_cache: [num_pages, page_size, H_kv, 2d]; block_table: int32
     [S, max_pages]; plan: extend_plan's.  Rows behind the last request are left as they are in `out`."""
-    _need(q.dim() == 4 and q.shape[2] == 2 and q.dtype == torch.bfloat16, "q must be bfloat16 [T, H, 2, d]")
-    T, H, _, d = q.shape
+    T, H, d = _rows(q)
     num_pages, page_size, H_kv = _cache_shapes(k_cache, v_cache, d, q.dtype)
     _need((T, H, H_kv, d) == (plan.T, plan.H, plan.H_kv, plan.d), "the plan was made for other sizes")
-    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == plan.S,
-          "block_table must be int32 [S, max_pages] with the plan's S")
+    bs = block_table.shape
+    if block_table.dtype is not torch.int32 or len(bs) != 2 or bs[0] != plan.S:
+        raise ValueError("block_table must be int32 [S, max_pages] with the plan's S")
     _scalar_f32("lam", lam)
     _f32("rms_w", rms_w, 2 * d)
     if out is None:
@@ -659,10 +672,10 @@ def diffattn_extend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if workspace is None:
         workspace = torch.empty(max(extend_workspace_size(plan), 16), dtype=torch.uint8, device=q.device)
     _launch("diffattn_extend", (q, k_cache, v_cache, block_table, plan.buf, lam, rms_w, workspace, out),
-            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1], num_pages, page_size,
-            _ptr(plan.buf), plan.buf.numel() * plan.buf.element_size(), plan.S, T, H, H_kv, d, plan.max_new,
-            _ptr(lam), float(lambda_init), _ptr(rms_w), float(eps), int(mode), _ptr(out), _ptr(workspace),
-            workspace.numel() * workspace.element_size())
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), bs[1], num_pages, page_size,
+            plan.buf.data_ptr(), plan.buf.nbytes, plan.S, T, H, H_kv, d, plan.max_new, lam.data_ptr(),
+            float(lambda_init), rms_w.data_ptr(), float(eps), int(mode), out.data_ptr(), workspace.data_ptr(),
+            workspace.nbytes)
     return out
 
 
