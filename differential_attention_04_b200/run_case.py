@@ -1,4 +1,4 @@
-"""Run one prefill or decode case a few times (e.g. under a profiler).
+"""Run one case a few times (e.g. under a profiler).
 
   python -m differential_attention_04_b200.run_case prefill --B 2 --N 4096 --H 12 --d 128 --causal 1 --iters 3
   python -m differential_attention_04_b200.run_case prefill --qk8 1 ...   (e4m3 queries/keys: quantise + forward;
@@ -8,6 +8,9 @@
   python -m differential_attention_04_b200.run_case proj --B 1 --N 4096 --H 12 --d 128 --dmodel 3072 --iters 3
                                                                           (QKV projection + RoPE, then output projection)
   python -m differential_attention_04_b200.run_case decode --S 64 --H 12 --lmin 1024 --lmax 4096 --iters 3
+  python -m differential_attention_04_b200.run_case serve --S 64 --H 12 --Hkv 12 --new 1 --page 64 --lmin 1024 --lmax 4096
+                                                                          (a step over a paged cache: page step,
+                                                                           schedule, cache write, attention)
 
 Inputs come from the seeded generators in ``workloads``; the output is not
 checked here (the tests do that).  Prints the CUDA-event time of each launch.
@@ -25,7 +28,7 @@ from .build import build
 
 def main(argv=None):
     ap = argparse.ArgumentParser()
-    ap.add_argument("kind", choices=["prefill", "decode", "bwd", "proj"])
+    ap.add_argument("kind", choices=["prefill", "decode", "bwd", "proj", "serve"])
     ap.add_argument("--B", type=int, default=2)
     ap.add_argument("--N", type=int, default=4096)
     ap.add_argument("--H", type=int, default=12)
@@ -39,6 +42,9 @@ def main(argv=None):
     ap.add_argument("--S", type=int, default=64)
     ap.add_argument("--lmin", type=int, default=1024)
     ap.add_argument("--lmax", type=int, default=4096)
+    ap.add_argument("--Hkv", type=int, default=12)
+    ap.add_argument("--new", type=int, default=1)
+    ap.add_argument("--page", type=int, default=64)
     ap.add_argument("--iters", type=int, default=3)
     ap.add_argument("--seed", type=int, default=0)
     a = ap.parse_args(argv)
@@ -85,6 +91,19 @@ def main(argv=None):
         def run():
             api.qkv_proj(inp.x, inp.w_qkv, a.B, a.N, a.H, a.d, table, out=qkv)
             api.out_proj(qkv[2], inp.w_o, out=y)
+    elif a.kind == "serve":
+        inp = wl.make_serve(a.S, a.H, a.Hkv, a.d, a.lmin, a.lmax, a.new, a.page, seed=a.seed, device=dev)
+        lam = api.diffattn_lambda(inp.lq1, inp.lk1, inp.lq2, inp.lk2, inp.lambda_init)
+        table = api.rope_table(a.lmax + a.new, a.d)
+        pool_out, T = torch.empty_like(inp.pool), inp.q.shape[0]
+
+        def run():
+            cu, kv, pos, slots, _ = api.paged_step(inp.ctx_lens, inp.new_lens, inp.block_table, inp.free_pages, inp.pool,
+                                                   inp.page_size, T, pool_out=pool_out)
+            plan = api.extend_plan(cu, kv, T, a.H, a.Hkv, a.d, inp.max_new)
+            q = api.kv_append(inp.q, inp.k, inp.v, pos, slots, table, inp.k_cache, inp.v_cache)
+            return api.diffattn_extend(q, inp.k_cache, inp.v_cache, inp.block_table, plan, lam, inp.lambda_init,
+                                       inp.rms_w, inp.eps)
     else:
         inp = wl.make_decode(a.S, a.H, a.d, a.lmin, a.lmax, seed=a.seed, device=dev)
         lam = api.diffattn_lambda(inp.lq1, inp.lk1, inp.lq2, inp.lk2, inp.lambda_init)

@@ -23,6 +23,9 @@ no dataset or trained weight is used):
   * Decode: per-sequence KV length L_s ~ U{lmin .. lmax} from
     ``numpy.random.default_rng(seed).integers(lmin, lmax + 1, S)``; sequences
     packed back to back; the cache includes the current token.
+  * Serving step: per-request cached length ~ U{lmin .. lmax} and new tokens
+    ~ U{1 .. new} from the same generator; the requests' pages a random
+    permutation of the pool, a ring of free pages for what the step takes.
 """
 from __future__ import annotations
 
@@ -186,3 +189,49 @@ def make_proj(B, N, d_model, H, d, seed=0, device="cpu") -> ProjInputs:
 
 def make_proj_case(name: str, seed=0, device="cpu") -> ProjInputs:
     return make_proj(seed=seed, device=device, **PROJ_CASES[name])
+
+
+@dataclass
+class ServeInputs:
+    q: torch.Tensor            # [T, H, 2, d], the new tokens' rows before rotation
+    k: torch.Tensor            # [T, H_kv, 2, d]
+    v: torch.Tensor            # [T, H_kv, 2d]
+    k_cache: torch.Tensor      # [num_pages, page_size, H_kv, 2, d]
+    v_cache: torch.Tensor      # [num_pages, page_size, H_kv, 2d]
+    ctx_lens: torch.Tensor     # int32 [S], cached before the step
+    new_lens: torch.Tensor     # int32 [S]
+    block_table: torch.Tensor  # int32 [S, max_pages]; -1 behind the cached pages
+    free_pages: torch.Tensor   # int32 ring
+    pool: torch.Tensor         # int32 [2]
+    page_size: int
+    max_new: int
+    lq1: torch.Tensor
+    lk1: torch.Tensor
+    lq2: torch.Tensor
+    lk2: torch.Tensor
+    rms_w: torch.Tensor
+    lambda_init: float
+    eps: float
+
+
+def make_serve(S, H, H_kv, d, lmin, lmax, new=1, page_size=64, lambda_init=0.5, w="normal", eps=EPS, seed=0,
+               device="cpu") -> ServeInputs:
+    rng = np.random.default_rng(seed)
+    ctx, n = rng.integers(lmin, lmax + 1, S), rng.integers(1, new + 1, S)
+    held, want = -(-ctx // page_size), -(-(ctx + n) // page_size)
+    num_pages, T = int(want.sum()), int(n.sum())
+    ids = rng.permutation(num_pages)
+    table = np.full((S, int(want.max())), -1)
+    for s, first in enumerate(np.cumsum(held) - held):
+        table[s, :held[s]] = ids[first:first + held[s]]
+    free = np.full(num_pages, -1)
+    free[:num_pages - int(held.sum())] = ids[int(held.sum()):]
+    gen = torch.Generator(device=device)
+    gen.manual_seed(seed)
+    bf = torch.bfloat16
+    rows = [_randn(shape, gen, device, bf) for shape in ((T, H, 2, d), (T, H_kv, 2, d), (T, H_kv, 2 * d))]
+    caches = [_randn((num_pages, page_size, H_kv) + tail, gen, device, bf) for tail in ((2, d), (2 * d,))]
+    lam, wv = _lambda_and_w(gen, device, d, w)
+    i32 = lambda x: torch.as_tensor(np.asarray(x), dtype=torch.int32, device=device)
+    return ServeInputs(*rows, *caches, i32(ctx), i32(n), i32(table), i32(free), i32([0, num_pages - held.sum()]),
+                       page_size, int(n.max()), *lam, wv, float(lambda_init), float(eps))

@@ -628,3 +628,11 @@ def test_serving_matches_the_dense_prefill(H, Hkv, d, page):
     assert pool.tolist()[1] == pages - sum(held) and ctx.tolist() == total
     used = [int(p) for s, n in enumerate(held) for p in bt[s, :n]]
     assert len(set(used)) == len(used)
+
+
+@pytest.mark.parametrize("args", [("--S", "9", "--H", "4", "--Hkv", "2", "--lmin", "1", "--lmax", "300", "--new", "50"),
+                                  ("--S", "3", "--H", "2", "--Hkv", "2", "--d", "64", "--lmin", "10", "--lmax", "900")])
+def test_serve_command(args, capsys):
+    from differential_attention_04_b200 import run_case
+    run_case.main(["serve", "--iters", "2", "--page", "16", *args])
+    assert capsys.readouterr().out.count("serve iter") == 2
