@@ -80,7 +80,7 @@ struct Bars {
   uint64_t mma_done;
   uint64_t exch_full, peer_ready, ss_full, epi_free;
   uint32_t tmem_base;
-  int abort;
+  volatile int abort;
 };
 static_assert(sizeof(Bars) <= 256, "barriers");
 
@@ -459,9 +459,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         continue;
       }
+      // After an abort nothing is exchanged any more (the waits for a partner
+      // that is gone would each run out); the four warps decide alike.
+      if (named_bar_or(1, 128, !sm_ok || bars->abort)) {
+        sm_ok = false;
+        named_bar_arrive(2, 160);
+        continue;
+      }
       // Both V stages are free of this segment's PV products: announce that
       // this CTA's receive buffer is ready, with the exchange barrier armed first.
-      named_bar_sync(1, 128);
       if (tid == 128) {
         mbar_arrive_expect_tx(&bars->exch_full, C::EXCH_BYTES);
         mbar_arrive_expect_tx(&bars->ss_full, kBM * 4);  // the partner's sums of squares, by st.async

@@ -99,6 +99,20 @@ struct TileBoxes {
   }
 };
 
+// Barrier over `count` threads that tells all of them whether any brought `x`.
+__device__ __forceinline__ bool named_bar_or(uint32_t id, uint32_t count, bool x) {
+  uint32_t y;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "bar.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(y)
+      : "r"(id), "r"(count), "r"(x ? 1u : 0u)
+      : "memory");
+  return y != 0;
+}
+
 // Zeros over the rows of a V tile ([64-channel block][128 rows][128 bytes])
 // behind its live ones, by one warp; the product reads them through the async proxy.
 __device__ __forceinline__ void clear_v_rows(uint8_t* tile, int blocks, int live, int lane) {

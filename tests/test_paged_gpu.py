@@ -426,6 +426,24 @@ def test_extend_is_repeatable_and_shares_its_plan():
         assert torch.equal(o, want)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_extend_forced_timeout_is_reported_and_context_survives(d):
+    """Every wait of the many-row kernels is bounded: with a limit of 1 ns they give up, say so and return."""
+    new, kv = [200, 64, 300], [700, 300, 300]
+    q, kc, vc, table, cu, plan, lam, w = _plain(new, kv, 3, 3, d, 16)
+    assert api.device_status() == api.OK
+    api.set_wait_limit_ns(1)
+    try:
+        api.diffattn_extend(q, kc, vc, i32(table), plan, lam, 0.4, w)
+        torch.cuda.synchronize()
+    finally:
+        api.set_wait_limit_ns(0)
+    assert api.device_status() == api.ERR_TIMEOUT
+    out = api.diffattn_extend(q, kc, vc, i32(table), plan, lam, 0.4, w)
+    assert api.device_status() == api.OK
+    _check(out, q, kc, vc, table, cu, kv, float(lam), w)
+
+
 def test_extend_offsets_behind_32_bits():
     """Pages behind 2^31 elements and 2^32 bytes of the cache."""
     Hkv, d, page = 4, 128, 64
