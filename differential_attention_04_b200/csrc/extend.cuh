@@ -29,7 +29,7 @@
 namespace diffattn {
 
 constexpr int kUnit = 128;
-constexpr int kNarrowRows = 8;
+constexpr int kNarrowRows = 16;
 constexpr int kWideRows = 128;
 // What an item costs beside its units, in units, from times of 74 requests of
 // 128 rows over 128 and 640 keys: 12 and 20 thousand cycles against 3.7 and 2.8

@@ -1,9 +1,9 @@
-// Attention of requests with at most 8 query rows per key head (single tokens,
+// Attention of requests with at most 16 query rows per key head (single tokens,
 // drafted tokens, small groups of shared heads) over a paged cache.
 //
 // HBM-bound: 8 d bytes of K and V per key and key head against 12 d flops per
-// row.  All 8 rows go through the matrix units at once, so the arithmetic does
-// not grow with the rows: with keys and channels as the M dimension of
+// row.  Eight rows go through the matrix units at once, so the arithmetic hardly
+// grows with the rows: with keys and channels as the M dimension of
 // m16n8k16 (S^T = K Q^T, O^T = V^T P^T) the rows are the N = 8 columns.  The
 // warp-level instruction is taken on purpose: tcgen05 has M = 128 and would
 // put P through shared memory, and the kernel needs a fraction of the
@@ -12,8 +12,10 @@
 // P enters as the sum of two bf16, the rounded weight and the remainder of the
 // rounding: one bf16 alone adds as much error to the output as the output's own
 // rounding (relative 2-norm 0.0026 against 0.0017).  With up to four rows the
-// remainders take the four free columns, at no cost; with five to eight they
-// are a second product into the same sums.
+// remainders take the four free columns, at no cost; with more they are a second
+// product into the same sums.  Nine to sixteen rows take two column tiles (as
+// tiles of 128 rows on the tensor cores, 16 rows over 32 x 2000 tokens and 16
+// heads took 250 us at d = 128 and 147 at d = 64; here 205 and 125).
 //
 // Two CTAs of two pairs of warps per SM take a contiguous range of the step's
 // units of 128 keys each (extend.cuh).  Within a unit the pairs take turns of
@@ -65,7 +67,7 @@ struct Narrow {
   static constexpr int STAGES = 3;                      // 48 KB a pair
   static constexpr int PITCH = DV + 4;                  // floats of a row of the merge buffer (no bank conflicts)
   static constexpr int OFF_BUF = kPairs * STAGES * STAGE;
-  static constexpr int SMEM = OFF_BUF + kPairs * kNarrowRows * PITCH * 4;
+  static constexpr int SMEM = OFF_BUF + kPairs * 8 * PITCH * 4;  // 8 rows of one map, or 4 of both, at a time
   static_assert(2 * (SMEM + 1024 + 512) <= 233472, "shared memory of two CTAs");
 };
 
@@ -123,13 +125,15 @@ struct Cursor {
 
 // one_unit: the block table holds at most kUnit keys, so a unit behind an
 // item's first has none, and the first is the whole item.
-template <int D>
+// NT: columns of 8 rows that an item may have (the host's bound of new tokens
+// says which; a kernel for 16 rows has no registers to spare).
+template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, 2) extend_narrow_kernel(const ExtendArgs a, float* recs, int page_shift,
                                                                     int max_keys, int one_unit, int* status) {
   using C = Narrow<D>;
-  constexpr int DV = C::DV, KS = D / 16, CT = DV / 16, R8 = kNarrowRows, SL = C::SL;
+  constexpr int DV = C::DV, KS = D / 16, CT = DV / 16, RT = 8 * NT, SL = C::SL;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float s_m[kPairs][2][R8], s_l[kPairs][2][R8], s_ss[2 * kPairs][R8];
+  __shared__ float s_m[kPairs][2][RT], s_l[kPairs][2][RT], s_ss[2 * kPairs][RT];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, pair = warp & (kPairs - 1), map = warp / kPairs;
   if (!plan_fits(a.plan, a.n, status)) return;
   const PlanView pv = plan_view(a.plan, a.n, 0);
@@ -194,16 +198,20 @@ __global__ void __launch_bounds__(kThreads, 2) extend_narrow_kernel(const Extend
   cur.unit = st.unit;
   cur.open(pv.narrow);
   // the queries of an item as the operand of S^T (this map's)
-  uint32_t qf[KS][2];
+  uint32_t qf[NT][KS][2];
   auto load_q = [&](const Cursor& it) {
-    const int R = it.rq.n * G, r = (lane >> 2) & (R <= R8 / 2 ? 3 : 7);
-    const uint32_t* qp =
-        static_cast<const uint32_t*>(a.q) +
-        ((static_cast<size_t>(it.rq.q0 + (r < R ? r / G : 0)) * H + it.hk * G + r % G) * DV + map * D) / 2 + (lane & 3);
+    const int R = it.rq.n * G;
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      qf[k][0] = r < R ? qp[8 * k] : 0u;
-      qf[k][1] = r < R ? qp[8 * k + 4] : 0u;
+    for (int t = 0; t < NT; ++t) {
+      const int r = 8 * t + ((lane >> 2) & (R <= 4 ? 3 : 7));
+      const uint32_t* qp =
+          static_cast<const uint32_t*>(a.q) +
+          ((static_cast<size_t>(it.rq.q0 + (r < R ? r / G : 0)) * H + it.hk * G + r % G) * DV + map * D) / 2 + (lane & 3);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        qf[t][k][0] = r < R ? qp[8 * k] : 0u;
+        qf[t][k][1] = r < R ? qp[8 * k + 4] : 0u;
+      }
     }
   };
   load_q(cur);
@@ -212,30 +220,36 @@ __global__ void __launch_bounds__(kThreads, 2) extend_narrow_kernel(const Extend
     const int take = min(left, cur.units - cur.unit);
     const bool begins = cur.unit == 0, whole = begins && (take == cur.units || one_unit);
     const int R = cur.rq.n * G;
-    const bool dup = R <= R8 / 2;  // columns 4 .. 7 hold rows 0 .. 3 again, with the remainders of their weights
+    const bool dup = R <= 4;  // columns 4 .. 7 hold rows 0 .. 3 again, with the remainders of their weights
     const int L = min(cur.rq.L, max_keys);
     if (cur.rq.L > max_keys && tid == 0) atomicCAS(status, 0, 6);
     // the item behind this one: its request is read now and its queries before the merge, so that neither is waited for
     Cursor nx = cur;
     const bool more = left > take;
     if (more) nx.next(pv.narrow, H_kv);
-    // this thread's two columns of S^T and O^T and the last keys that their rows see
-    int lim[2];
+    // this thread's columns of S^T and O^T and the last keys that their rows see
+    int lim[NT][2];
+    float o[NT][CT][4], mx[NT][2], l[NT][2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int r = (2 * (lane & 3) + j) & (dup ? 3 : 7);
-      lim[j] = causal && r < R ? min(cur.rq.L - cur.rq.n + r / G, L - 1) : L - 1;
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = 8 * t + ((2 * (lane & 3) + j) & (dup ? 3 : 7));
+        lim[t][j] = causal && r < R ? min(cur.rq.L - cur.rq.n + r / G, L - 1) : L - 1;
+        mx[t][j] = -INFINITY;
+        l[t][j] = 0.f;
+      }
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[t][c][i] = 0.f;
     }
     const int lim_min = causal ? min(cur.rq.L - cur.rq.n, L - 1) : L - 1;
     const bool rest = dup && (lane & 2);  // this thread's columns are remainders
-    float o[CT][4], mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-#pragma unroll
-    for (int c = 0; c < CT; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[c][i] = 0.f;
-    // one loop for each way, so that neither carries the other's registers
-    auto steps_of = [&](auto dup_c) {
+    // one loop for each way, so that none carries another's registers
+    auto steps_of = [&](auto dup_c, auto nt_c) {
       constexpr bool DUP = decltype(dup_c)::value;
+      constexpr int NN = decltype(nt_c)::value;
       for (int i = 0; i < SPU * take; ++i, ++step) {
         cp_wait<C::STAGES - 2>();
         named_bar_sync(1 + pair, 64);  // both halves of the step are here, and the step before it has been read
@@ -245,173 +259,200 @@ __global__ void __launch_bounds__(kThreads, 2) extend_narrow_kernel(const Extend
           const uint32_t kb = ring + (step % C::STAGES) * C::STAGE;
           const int lr = lane & 7, mi = lane >> 3;
           // S^T: keys x rows
-          float s[SL][4], t[2] = {-INFINITY, -INFINITY};
+          float s[SL][NN][4], tm[NN][2];
+#pragma unroll
+          for (int t = 0; t < NN; ++t) tm[t][0] = tm[t][1] = -INFINITY;
 #pragma unroll
           for (int x = 0; x < SL; ++x) {
             const uint32_t base = kb + x * C::SLICE + (lr + (mi & 1) * 8) * C::ROW;
-            float e[2][4] = {};  // two chains of products
+            float e[2][NN][4] = {};  // two chains of products
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
               uint32_t f[4];
               ldsm4(f, base + (((map * (D / 8) + 2 * k + (mi >> 1)) ^ lr) << 4));
-              mma(e[k & 1], f, qf[k][0], qf[k][1]);
+#pragma unroll
+              for (int t = 0; t < NN; ++t) mma(e[k & 1][t], f, qf[t][k][0], qf[t][k][1]);
             }
+            const int key0 = first + kPairs * kSlice * x, k_lo = key0 + (lane >> 2);
+            const bool mask = key0 + kSlice - 1 > lim_min;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[x][j] = (e[0][j] + e[1][j]) * sc;
-            if (first + kPairs * kSlice * x + kSlice - 1 > lim_min) {
-              const int k_lo = first + kPairs * kSlice * x + (lane >> 2);
+            for (int t = 0; t < NN; ++t) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (k_lo + (j >> 1) * 8 > lim[j & 1]) s[x][j] = -INFINITY;
+              for (int j = 0; j < 4; ++j) {
+                s[x][t][j] = (e[0][t][j] + e[1][t][j]) * sc;
+                if (mask && k_lo + (j >> 1) * 8 > lim[t][j & 1]) s[x][t][j] = -INFINITY;
+              }
+#pragma unroll
+              for (int j = 0; j < 2; ++j) tm[t][j] = fmaxf(tm[t][j], fmaxf(s[x][t][j], s[x][t][j + 2]));
             }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) t[j] = fmaxf(t[j], fmaxf(s[x][j], s[x][j + 2]));
           }
+          bool grow = false;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            t[j] = fmaxf(t[j], __shfl_xor_sync(0xffffffffu, t[j], 4));
-            t[j] = fmaxf(t[j], __shfl_xor_sync(0xffffffffu, t[j], 8));
-            t[j] = fmaxf(t[j], __shfl_xor_sync(0xffffffffu, t[j], 16));
-          }
-          if (__any_sync(0xffffffffu, t[0] > mx[0] + kLazy || t[1] > mx[1] + kLazy)) {
-            float al[2];
+          for (int t = 0; t < NN; ++t)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float mn = fmaxf(mx[j], t[j]);
-              al[j] = mn == -INFINITY ? 1.f : fast_exp2(mx[j] - mn);
-              mx[j] = mn;
-              l[j] *= al[j];
+              float& m = tm[t][j];
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+              grow |= m > mx[t][j] + kLazy;
             }
+          if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-            for (int c = 0; c < CT; ++c) {
+            for (int t = 0; t < NN; ++t) {
+              float al[2];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) o[c][j] *= al[j & 1];
+              for (int j = 0; j < 2; ++j) {
+                const float mn = fmaxf(mx[t][j], tm[t][j]);
+                al[j] = mn == -INFINITY ? 1.f : fast_exp2(mx[t][j] - mn);
+                mx[t][j] = mn;
+                l[t][j] *= al[j];
+              }
+#pragma unroll
+              for (int c = 0; c < CT; ++c) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[t][c][j] *= al[j & 1];
+              }
             }
           }
 #pragma unroll
           for (int x = 0; x < SL; ++x) {
             if (x > 0 && first + kPairs * kSlice * x >= L) break;
-            uint32_t pb[2], pl[2];
+            uint32_t pb[NN][2], pl[NN][2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float p0 = fast_exp2(s[x][2 * j] - (mx[0] == -INFINITY ? 0.f : mx[0]));
-              const float p1 = fast_exp2(s[x][2 * j + 1] - (mx[1] == -INFINITY ? 0.f : mx[1]));
-              l[0] += p0;
-              l[1] += p1;
-              const uint32_t hi = pack_bf16x2(p0, p1);
-              const uint32_t lo = pack_bf16x2(p0 - bf16lo_to_f32(hi), p1 - bf16hi_to_f32(hi));
-              pb[j] = transpose8x8(DUP && rest ? lo : hi);
-              pl[j] = lo;
-            }
+            for (int t = 0; t < NN; ++t)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const float p0 = fast_exp2(s[x][t][2 * j] - (mx[t][0] == -INFINITY ? 0.f : mx[t][0]));
+                const float p1 = fast_exp2(s[x][t][2 * j + 1] - (mx[t][1] == -INFINITY ? 0.f : mx[t][1]));
+                l[t][0] += p0;
+                l[t][1] += p1;
+                const uint32_t hi = pack_bf16x2(p0, p1);
+                const uint32_t lo = pack_bf16x2(p0 - bf16lo_to_f32(hi), p1 - bf16hi_to_f32(hi));
+                pb[t][j] = transpose8x8(DUP && rest ? lo : hi);
+                if constexpr (!DUP) pl[t][j] = transpose8x8(lo);
+              }
             // O^T += V^T P^T: channels x rows
             const uint32_t base = kb + x * C::SLICE + (kSlice + lr + (mi >> 1) * 8) * C::ROW;
-            if constexpr (DUP) {
 #pragma unroll
-              for (int c = 0; c < CT; ++c) {
-                uint32_t f[4];
-                ldsm4t(f, base + (((2 * c + (mi & 1)) ^ lr) << 4));
-                mma(o[c], f, pb[0], pb[1]);
-              }
-            } else {
-              pl[0] = transpose8x8(pl[0]);
-              pl[1] = transpose8x8(pl[1]);
+            for (int c = 0; c < CT; ++c) {
+              uint32_t f[4];
+              ldsm4t(f, base + (((2 * c + (mi & 1)) ^ lr) << 4));
 #pragma unroll
-              for (int c = 0; c < CT; ++c) {
-                uint32_t f[4];
-                ldsm4t(f, base + (((2 * c + (mi & 1)) ^ lr) << 4));
-                mma(o[c], f, pb[0], pb[1]);
-                mma(o[c], f, pl[0], pl[1]);
+              for (int t = 0; t < NN; ++t) {
+                mma(o[t][c], f, pb[t][0], pb[t][1]);
+                if constexpr (!DUP) mma(o[t][c], f, pl[t][0], pl[t][1]);
               }
             }
           }
         }
       }
     };
+    using One = std::integral_constant<int, 1>;
     if (dup)
-      steps_of(std::true_type{});
+      steps_of(std::true_type{}, One{});
+    else if (NT == 1 || R <= 8)
+      steps_of(std::false_type{}, One{});
     else
-      steps_of(std::false_type{});
+      steps_of(std::false_type{}, std::integral_constant<int, NT>{});
     if (more) load_q(nx);
 
     // ------------------------------------------------- merge of the pairs --
     // Every warp leaves its maxima, sums and unnormalised O^T; the thread that
-    // finishes a channel takes the four pairs' to their common maximum itself.
-    // With up to four rows both maps fit the buffer (rows 0 .. 3 and 4 .. 7)
-    // and one barrier does; with more the maps go through it one by one.
+    // finishes a channel takes the pairs' to their common maximum itself.  With
+    // up to four rows both maps fit the buffer (rows 0 .. 3 and 4 .. 7) and one
+    // barrier does; with more, eight rows of a map go through it at a time.
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float x = l[j];
-      x += __shfl_xor_sync(0xffffffffu, x, 4);
-      x += __shfl_xor_sync(0xffffffffu, x, 8);
-      x += __shfl_xor_sync(0xffffffffu, x, 16);
-      if (lane < 4) {
-        s_l[pair][map][2 * lane + j] = x;
-        s_m[pair][map][2 * lane + j] = mx[j];
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float x = l[t][j];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        if (lane < 4) {
+          s_l[pair][map][8 * t + 2 * lane + j] = x;
+          s_m[pair][map][8 * t + 2 * lane + j] = mx[t][j];
+        }
       }
-    }
-    if (dup) {  // the weights' and their remainders' products
-#pragma unroll
-      for (int c = 0; c < CT; ++c)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[c][j] += __shfl_xor_sync(0xffffffffu, o[c][j], 2);
-    }
     // The item's record, for a part of it that the joining kernel reads.
-    float* rec = recs + (2 * blockIdx.x + (begins ? 1 : 0)) * record_floats(R8, D);
+    float* rec = recs + (2 * blockIdx.x + (begins ? 1 : 0)) * record_floats(kNarrowRows, D);
     const bool part = !whole && !(one_unit && !begins);
     // a thread finishes channels tid, tid + kThreads, ... of every row
     constexpr int E = DV / kThreads;
-    float y[R8][E];
+    float y[RT][E];
 #pragma unroll
-    for (int r = 0; r < R8; ++r)
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int e = 0; e < E; ++e) y[r][e] = 0.f;
-    for (int phase = 0; phase < (dup ? 1 : 2); ++phase) {
-      if (phase) __syncthreads();  // the buffer's first map has been read
-      if (dup || map == phase) {
-        float* to = buf + static_cast<size_t>(pair * R8 + (dup ? 4 * map : 0)) * C::PITCH + (lane >> 2);
+    auto leave = [&](const float (&x)[CT][4], int row0, int rows) {  // this thread's columns below `rows`, from row0 on
+      float* to = buf + static_cast<size_t>(pair * 8 + row0) * C::PITCH + (lane >> 2);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int r = 2 * (lane & 3) + j;
-          if (r < R) {
+      for (int j = 0; j < 2; ++j) {
+        const int r = 2 * (lane & 3) + j;
+        if (r < rows) {
 #pragma unroll
-            for (int c = 0; c < CT; ++c) {
-              to[r * C::PITCH + 16 * c] = o[c][j];
-              to[r * C::PITCH + 16 * c + 8] = o[c][j + 2];
-            }
+          for (int c = 0; c < CT; ++c) {
+            to[r * C::PITCH + 16 * c] = x[c][j];
+            to[r * C::PITCH + 16 * c + 8] = x[c][j + 2];
           }
         }
       }
+    };
+    auto finish = [&](float (&z)[E], int r, int m, int at) {  // row r of map m, at row `at` of the buffer
+      float M = -INFINITY, sum = 0.f, f[kPairs];
+#pragma unroll
+      for (int w = 0; w < kPairs; ++w) M = fmaxf(M, s_m[w][m][r]);
+#pragma unroll
+      for (int w = 0; w < kPairs; ++w) {
+        f[w] = M == -INFINITY ? 0.f : fast_exp2(s_m[w][m][r] - M);
+        sum = fmaf(f[w], s_l[w][m][r], sum);
+      }
+      const float scale = sum > 0.f ? (m ? c2 : 1.f) / sum : 0.f;
+      if (part && tid == 0) *reinterpret_cast<float2*>(rec + 4 * r + 2 * m) = make_float2(M, sum);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float* b = buf + at * C::PITCH + tid + e * kThreads;
+        float x = 0.f;
+#pragma unroll
+        for (int w = 0; w < kPairs; ++w) x = fmaf(f[w], b[w * 8 * C::PITCH], x);
+        if (part) rec[4 * kNarrowRows + static_cast<size_t>(r) * 2 * DV + m * DV + tid + e * kThreads] = x;
+        z[e] = fmaf(x, scale, z[e]);
+      }
+    };
+    if (dup) {
+      // the weights' and their remainders' products
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[0][c][j] += __shfl_xor_sync(0xffffffffu, o[0][c][j], 2);
+      leave(o[0], 4 * map, R);
       __syncthreads();
 #pragma unroll
-      for (int r = 0; r < R8; ++r) {
+      for (int r = 0; r < 4; ++r) {
         if (r < R) {
-          for (int m = dup ? 0 : phase; m < (dup ? 2 : phase + 1); ++m) {
-            float M = -INFINITY, sum = 0.f, f[kPairs];
+          finish(y[r], r, 0, r);
+          finish(y[r], r, 1, 4 + r);
+        }
+      }
+    } else {
+      for (int m = 0; m < 2; ++m) {
 #pragma unroll
-            for (int w = 0; w < kPairs; ++w) M = fmaxf(M, s_m[w][m][r]);
+        for (int t = 0; t < NT; ++t) {
+          if (8 * t < R) {
+            if (m + t > 0) __syncthreads();  // the rows before these have been read
+            if (map == m) leave(o[t], 0, R - 8 * t);
+            __syncthreads();
 #pragma unroll
-            for (int w = 0; w < kPairs; ++w) {
-              f[w] = M == -INFINITY ? 0.f : fast_exp2(s_m[w][m][r] - M);
-              sum = fmaf(f[w], s_l[w][m][r], sum);
-            }
-            const float scale = sum > 0.f ? (m ? c2 : 1.f) / sum : 0.f;
-            if (part && tid == 0) *reinterpret_cast<float2*>(rec + 4 * r + 2 * m) = make_float2(M, sum);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-              const float* b = buf + (dup ? 4 * m + r : r) * C::PITCH + tid + e * kThreads;
-              float x = 0.f;
-#pragma unroll
-              for (int w = 0; w < kPairs; ++w) x = fmaf(f[w], b[w * R8 * C::PITCH], x);
-              if (part) rec[4 * R8 + static_cast<size_t>(r) * 2 * DV + m * DV + tid + e * kThreads] = x;
-              y[r][e] = fmaf(x, scale, y[r][e]);
-            }
+            for (int r = 0; r < 8; ++r)
+              if (8 * t + r < R) finish(y[8 * t + r], 8 * t + r, m, r);
           }
         }
       }
     }
     if (whole) {  // the same for the whole CTA
 #pragma unroll
-      for (int r = 0; r < R8; ++r) {
+      for (int r = 0; r < RT; ++r) {
         if (r < R) {
           float ss = 0.f;
 #pragma unroll
@@ -426,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 2) extend_narrow_kernel(const Extend
     __syncthreads();
     if (whole) {
 #pragma unroll
-      for (int r = 0; r < R8; ++r) {
+      for (int r = 0; r < RT; ++r) {
         if (r < R) {
           float ss = 0.f;
 #pragma unroll
@@ -448,12 +489,12 @@ __global__ void __launch_bounds__(kThreads, 2) extend_narrow_kernel(const Extend
   cp_wait<0>();
 }
 
-template <int D>
+template <int D, int NT>
 cudaError_t launch_d(const ExtendArgs& a, float* recs, DevCtl ctl, cudaStream_t stream) {
   static unsigned long long set_ctx[64] = {};
   if (ctl.dev < 0 || ctl.dev >= 64) return cudaErrorInvalidDevice;
   if (ctl.ctx == 0 || set_ctx[ctl.dev] != ctl.ctx) {
-    const cudaError_t e = cudaFuncSetAttribute(extend_narrow_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(extend_narrow_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                Narrow<D>::SMEM);
     if (e != cudaSuccess) return e;
     set_ctx[ctl.dev] = ctl.ctx;
@@ -462,14 +503,16 @@ cudaError_t launch_d(const ExtendArgs& a, float* recs, DevCtl ctl, cudaStream_t 
   while ((1 << shift) < a.page_size) ++shift;
   const long long keys = static_cast<long long>(a.max_pages) * a.page_size;
   const int max_keys = keys < kMaxKeys ? static_cast<int>(keys) : kMaxKeys;
-  extend_narrow_kernel<D><<<kNarrowWorkers, kThreads, Narrow<D>::SMEM, stream>>>(
+  extend_narrow_kernel<D, NT><<<kNarrowWorkers, kThreads, Narrow<D>::SMEM, stream>>>(
       a, recs, shift, max_keys, keys <= kUnit && !wide_possible(a.n), ctl.status);
   return cudaGetLastError();
 }
 }  // namespace
 
 cudaError_t launch_extend_narrow(const ExtendArgs& a, float* recs, DevCtl ctl, cudaStream_t stream) {
-  return a.n.d == 128 ? launch_d<128>(a, recs, ctl, stream) : launch_d<64>(a, recs, ctl, stream);
+  const bool few = static_cast<long long>(a.n.max_new) * (a.n.H / a.n.H_kv) <= 8;
+  if (a.n.d == 128) return few ? launch_d<128, 1>(a, recs, ctl, stream) : launch_d<128, 2>(a, recs, ctl, stream);
+  return few ? launch_d<64, 1>(a, recs, ctl, stream) : launch_d<64, 2>(a, recs, ctl, stream);
 }
 
 }  // namespace diffattn

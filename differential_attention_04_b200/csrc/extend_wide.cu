@@ -1,4 +1,4 @@
-// Attention of requests with more than 8 query rows per key head (chunks of
+// Attention of requests with more than 16 query rows per key head (chunks of
 // prompts, whole prompts, many heads sharing a key head) over a paged cache,
 // on the tensor cores, d = 128.
 //

@@ -1,4 +1,4 @@
-// Attention of requests with more than 8 query rows per key head over a paged
+// Attention of requests with more than 16 query rows per key head over a paged
 // cache, on the tensor cores, d = 64: one CTA computes both maps.
 //
 // Rows, pages, schedule and records are those of extend_wide.cu.  At d = 64
