@@ -25,32 +25,34 @@ __device__ __forceinline__ PlanSums plan_add(const PlanSums& a, const PlanSums& 
   return PlanSums{a.units + b.units, a.reqs + b.reqs, a.tiles + b.tiles, max(a.top, b.top)};
 }
 
-// Exclusive scan over the block (identity: zeros and the smallest int); `total` gets the block's.
+// Exclusive scan over the block (identity: zeros and the smallest int); `total`
+// gets the block's.  Every warp scans the warps' totals for itself.
 __device__ __forceinline__ PlanSums plan_scan(PlanSums v, PlanSums* sm, PlanSums& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  PlanSums x = v;
-  auto up = [](const PlanSums& a, int off) {
-    return PlanSums{__shfl_up_sync(0xffffffffu, a.units, off), __shfl_up_sync(0xffffffffu, a.reqs, off),
-                    __shfl_up_sync(0xffffffffu, a.tiles, off), __shfl_up_sync(0xffffffffu, a.top, off)};
+  auto inclusive = [&](PlanSums x) {
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const PlanSums o{__shfl_up_sync(0xffffffffu, x.units, off), __shfl_up_sync(0xffffffffu, x.reqs, off),
+                       __shfl_up_sync(0xffffffffu, x.tiles, off), __shfl_up_sync(0xffffffffu, x.top, off)};
+      if (lane >= off) x = plan_add(o, x);
+    }
+    return x;
+  };
+  auto of = [](const PlanSums& x, int from) {
+    return PlanSums{__shfl_sync(0xffffffffu, x.units, from), __shfl_sync(0xffffffffu, x.reqs, from),
+                    __shfl_sync(0xffffffffu, x.tiles, from), __shfl_sync(0xffffffffu, x.top, from)};
   };
   const PlanSums none{0, 0, 0, static_cast<int>(0x80000000)};
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const PlanSums o = up(x, off);
-    if (lane >= off) x = plan_add(o, x);
-  }
+  const PlanSums x = inclusive(v);
   if (lane == 31) sm[warp] = x;
   __syncthreads();
-  PlanSums before = none;
-  total = none;
-#pragma unroll 4
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    if (w == warp) before = total;
-    total = plan_add(total, sm[w]);
-  }
+  static_assert(kPlanThreads == 1024, "one total a lane");
+  const PlanSums w = inclusive(sm[lane]);
   __syncthreads();  // sm is reused
-  const PlanSums prev = up(x, 1);
-  return lane == 0 ? before : plan_add(before, prev);
+  total = of(w, 31);
+  const PlanSums last = of(w, max(warp - 1, 0)), prev = of(x, max(lane - 1, 0));
+  const PlanSums before = warp ? last : none;
+  return lane ? plan_add(before, prev) : before;
 }
 
 __device__ __forceinline__ int units_of(long long keys) {
@@ -84,6 +86,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
   long long* wpre = reinterpret_cast<long long*>(plan + lay.wide_pre);
   WideItem* items = reinterpret_cast<WideItem*>(plan + lay.items);
   __shared__ long long cut[2][kNarrowWorkers + 1];  // where the workers' ranges begin on the lines
+  __shared__ long long whole_cost[kNarrowWorkers];  // of a wide worker's whole items
   __shared__ int s_rounds;
   const int tid = threadIdx.x, lane = tid & 31;
   const int G = n.H / n.H_kv, tpt = kWideRows / G;
@@ -213,24 +216,22 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
   if (tid < W[1]) {
     long long cost;
     whole_items(rounds, U[1], cost);
-    cut[1][tid] = cost;
+    whole_cost[tid] = cost;
   }
   if (tid < W[0]) cut[0][tid] = tid * U[0] / W[0];
   __syncthreads();
-  if (tid == 0 && W[1] > 0) {
+  if (tid < W[1]) {
     // the line behind the whole items, cut where the workers' shares are used up
     long long at = U[1], used = 0;
     const long long done = static_cast<long long>(rounds) * W[1];
     if (done < nitems) {
-      const int x = items[done].tile, first = wide[x].first, cnt = wide[x].count;
-      at = wide_line(first) * n.H_kv + items[done].hk * (wide_line(first + cnt) - wide_line(first)) + wide_line(x) -
+      const WideItem it = items[done];
+      const int first = wide[it.tile].first, cnt = wide[it.tile].count;
+      at = wide_line(first) * n.H_kv + it.hk * (wide_line(first + cnt) - wide_line(first)) + wide_line(it.tile) -
            wide_line(first);
     }
-    for (int w = 0; w < W[1]; ++w) {
-      const long long took = cut[1][w];
-      cut[1][w] = at + w * U[1] / W[1] - used;
-      used += took;
-    }
+    for (int v = 0; v < tid; ++v) used += whole_cost[v];
+    cut[1][tid] = at + tid * U[1] / W[1] - used;
   }
   if (tid == 0) *head = PlanHeader{{W[0], W[1]}, causal, ntiles, n, kPlanMagic, rounds, {}};
   __syncthreads();
