@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
       nq = -1;
     }
     carry.top = max(carry.top, total.top);
-    const bool is_wide = static_cast<long long>(nq) * G > kNarrowRows;
+    const bool is_wide = static_cast<long long>(nq) * G > narrow_rows(n);
     v = PlanSums{0, 0, 0, static_cast<int>(0x80000000)};
     if (nq > 0 && !is_wide) {
       v.reqs = 1;
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kJoinThreads) extend_join_kernel(const ExtendA
   const int G = a.n.H / a.n.H_kv;
   const int tok0 = is_wide ? pv.wide[tl.at].tok0 : pv.narrow[tl.at].q0;
   const int R = (is_wide ? pv.wide[tl.at].ntok : pv.narrow[tl.at].n) * G;
-  const int rows = is_wide ? kWideRows : kNarrowRows;
+  const int rows = is_wide ? kWideRows : narrow_rows(a.n);
   const float* recs = is_wide ? wrecs : nrecs;
   const size_t rec = record_floats(rows, D);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kJoinThreads) extend_join_kernel(const ExtendA
 }
 
 size_t narrow_record_bytes(const ExtendShape& n) {
-  return 2 * kNarrowWorkers * record_floats(kNarrowRows, n.d) * sizeof(float);
+  return 2 * kNarrowWorkers * record_floats(narrow_rows(n), n.d) * sizeof(float);
 }
 }  // namespace
 

@@ -2,7 +2,7 @@
 // attention kernels and the kernel that joins split rows.
 //
 // A request's query rows are its new tokens times the G = H / H_kv query heads
-// that share a key head.  Requests of at most kNarrowRows rows are "narrow"
+// that share a key head.  Requests of at most narrow_rows rows are "narrow"
 // (extend_narrow.cu: memory-bound), the others "wide" (extend_wide*.cu: tiles of
 // up to 128 rows on the tensor cores).  An item is one (request, key head) of
 // the narrow class or one (row tile, key head) of the wide class; its work is
@@ -29,7 +29,6 @@
 namespace diffattn {
 
 constexpr int kUnit = 128;
-constexpr int kNarrowRows = 16;
 constexpr int kWideRows = 128;
 // What an item costs beside its units, in units, from times of 74 requests of
 // 128 rows over 128 and 640 keys: 12 and 20 thousand cycles against 3.7 and 2.8
@@ -85,9 +84,18 @@ struct PlanLayout {
   int max_tiles;  // row tiles of the wide class there can be
 };
 
-__host__ __device__ inline bool wide_possible(const ExtendShape& n) {
-  return static_cast<long long>(n.max_new) * (n.H / n.H_kv) > kNarrowRows;
+// The most rows of a request that the host's bound allows.
+__host__ __device__ inline long long most_rows(const ExtendShape& n) {
+  return static_cast<long long>(n.max_new) * (n.H / n.H_kv);
 }
+// Rows of the narrow class.  Two column tiles (9 to 16 rows) are 20% faster
+// than a 128-row tile, but the kernel that has them takes 7 to 10 us longer over
+// the single tokens of a step with chunks (mixed step 48 against 55 us), so they
+// are for steps that need no wide kernel.
+__host__ __device__ inline int narrow_rows(const ExtendShape& n) {
+  return most_rows(n) > 8 && most_rows(n) <= 16 ? 16 : 8;
+}
+__host__ __device__ inline bool wide_possible(const ExtendShape& n) { return most_rows(n) > 16; }
 
 __host__ __device__ inline PlanLayout plan_layout(const ExtendShape& n) {
   PlanLayout l;

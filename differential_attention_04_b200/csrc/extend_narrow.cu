@@ -13,9 +13,10 @@
 // rounding: one bf16 alone adds as much error to the output as the output's own
 // rounding (relative 2-norm 0.0026 against 0.0017).  With up to four rows the
 // remainders take the four free columns, at no cost; with more they are a second
-// product into the same sums.  Nine to sixteen rows take two column tiles (as
-// tiles of 128 rows on the tensor cores, 16 rows over 32 x 2000 tokens and 16
-// heads took 250 us at d = 128 and 147 at d = 64; here 205 and 125).
+// product into the same sums.  Nine to sixteen rows take two column tiles, in
+// steps that have no more (narrow_rows in extend.cuh).  As tiles of 128 rows on
+// the tensor cores, 16 rows over 32 x 2000 tokens and 16 heads took 250 us at
+// d = 128 and 147 at d = 64; here 205 and 124.
 //
 // Two CTAs of two pairs of warps per SM take a contiguous range of the step's
 // units of 128 keys each (extend.cuh).  Within a unit the pairs take turns of
@@ -376,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 2) extend_narrow_kernel(const Extend
         }
       }
     // The item's record, for a part of it that the joining kernel reads.
-    float* rec = recs + (2 * blockIdx.x + (begins ? 1 : 0)) * record_floats(kNarrowRows, D);
+    float* rec = recs + (2 * blockIdx.x + (begins ? 1 : 0)) * record_floats(RT, D);
     const bool part = !whole && !(one_unit && !begins);
     // a thread finishes channels tid, tid + kThreads, ... of every row
     constexpr int E = DV / kThreads;
@@ -416,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 2) extend_narrow_kernel(const Extend
         float x = 0.f;
 #pragma unroll
         for (int w = 0; w < kPairs; ++w) x = fmaf(f[w], b[w * 8 * C::PITCH], x);
-        if (part) rec[4 * kNarrowRows + static_cast<size_t>(r) * 2 * DV + m * DV + tid + e * kThreads] = x;
+        if (part) rec[4 * RT + static_cast<size_t>(r) * 2 * DV + m * DV + tid + e * kThreads] = x;
         z[e] = fmaf(x, scale, z[e]);
       }
     };
@@ -510,7 +511,7 @@ cudaError_t launch_d(const ExtendArgs& a, float* recs, DevCtl ctl, cudaStream_t 
 }  // namespace
 
 cudaError_t launch_extend_narrow(const ExtendArgs& a, float* recs, DevCtl ctl, cudaStream_t stream) {
-  const bool few = static_cast<long long>(a.n.max_new) * (a.n.H / a.n.H_kv) <= 8;
+  const bool few = narrow_rows(a.n) == 8;
   if (a.n.d == 128) return few ? launch_d<128, 1>(a, recs, ctl, stream) : launch_d<128, 2>(a, recs, ctl, stream);
   return few ? launch_d<64, 1>(a, recs, ctl, stream) : launch_d<64, 2>(a, recs, ctl, stream);
 }
