@@ -75,8 +75,7 @@ __device__ __forceinline__ int last_at_most(int lo, int hi, long long u, F pre) 
 // it once for all layers.
 __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __restrict__ cu,
                                                                    const int* __restrict__ kvl, ExtendShape n,
-                                                                   int causal, char* plan,
-                                                                   int* status) {
+                                                                   int causal, char* plan, int* status) {
   __shared__ PlanSums sm[kPlanThreads / 32];
   const PlanLayout lay = plan_layout(n);
   PlanHeader* head = reinterpret_cast<PlanHeader*>(plan);
@@ -105,7 +104,8 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
       // offsets must not fall below an earlier one: then no two requests share rows, and
       // the row tiles fit their list
       v.top = q0;
-      nq = q0 < 0 || end < q0 || end > n.T || L < 0 || L > kMaxKeys || end - q0 > n.max_new ? -1 : static_cast<int>(end - q0);
+      const bool fits = q0 >= 0 && end >= q0 && end <= n.T && L >= 0 && L <= kMaxKeys && end - q0 <= n.max_new;
+      nq = fits ? static_cast<int>(end - q0) : -1;
     }
     // whether it fits is only known with the largest earlier offset, so that is scanned first
     PlanSums total;
@@ -287,7 +287,8 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
         // its first unit.
         if (u1 < all && x1.unit > 0) {
           const int owner = last_at_most(0, w, x1.cost + ic, [&](int v) { return cut[c][v]; });
-          const int end = last_at_most(w + 1, W[c] - 1, x1.cost + ic + x1.e - x1.b - 1, [&](int v) { return cut[c][v]; });
+          const int end =
+              last_at_most(w + 1, W[c] - 1, x1.cost + ic + x1.e - x1.b - 1, [&](int v) { return cut[c][v]; });
           tl = WorkTail{index(x1), x1.hk, end - owner + 1, w - owner};
         }
       }
@@ -493,7 +494,8 @@ size_t extend_workspace_bytes(const ExtendShape& n) {
 
 cudaError_t launch_extend_plan(const int* cu_q, const int* kv_lens, const ExtendShape& n, int causal, void* plan,
                                DevCtl ctl, cudaStream_t stream) {
-  extend_plan_kernel<<<1, kPlanThreads, 0, stream>>>(cu_q, kv_lens, n, causal ? 1 : 0, static_cast<char*>(plan), ctl.status);
+  extend_plan_kernel<<<1, kPlanThreads, 0, stream>>>(cu_q, kv_lens, n, causal ? 1 : 0, static_cast<char*>(plan),
+                                                     ctl.status);
   return cudaGetLastError();
 }
 
@@ -503,7 +505,8 @@ cudaError_t launch_extend(const ExtendArgs& a, DevCtl ctl, cudaStream_t stream) 
   const bool wide = wide_possible(a.n);
   cudaError_t e = launch_extend_narrow(a, nrecs, ctl, stream);
   if (e != cudaSuccess) return e;
-  if (wide) e = a.n.d == 64 ? launch_extend_wide64(a, wrecs, ctl, stream) : launch_extend_wide128(a, wrecs, ctl, stream);
+  if (wide)
+    e = a.n.d == 64 ? launch_extend_wide64(a, wrecs, ctl, stream) : launch_extend_wide128(a, wrecs, ctl, stream);
   if (e != cudaSuccess) return e;
   // no item can be split where every request's keys fit one unit
   if (!wide && static_cast<long long>(a.max_pages) * a.page_size <= kUnit) return cudaSuccess;
