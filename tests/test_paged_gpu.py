@@ -519,6 +519,55 @@ def test_extend_larger(d, new, kv, H, Hkv, page, causal):
     _check_on_device(out, q, kc, vc, table, cu, kv, float(lam), w, causal)
 
 
+_rng = np.random.default_rng(2025)
+RANDOM_STEPS = []
+for _ in range(16):
+    _G, _d, _page = int(_rng.choice([1, 1, 2, 3, 5, 7])), int(_rng.choice([64, 128])), int(_rng.choice([16, 32, 64, 256]))
+    _top = int(_rng.choice([2, 9, 17, 300]))
+    _new = [int(x) for x in _rng.integers(0, _top, int(_rng.integers(1, 14)))]
+    _kv = [int(n + (0 if _rng.random() < 0.3 else _rng.integers(0, 1500))) for n in _new]
+    RANDOM_STEPS.append((_d, _new, _kv, _G * int(_rng.integers(1, 5)), _G, _page, bool(_rng.random() < 0.8)))
+
+
+@pytest.mark.parametrize("d,new,kv,H,G,page,causal", RANDOM_STEPS)
+def test_extend_random_steps(d, new, kv, H, G, page, causal):
+    cu = np.concatenate([[0], np.cumsum(new)])
+    T = int(cu[-1]) + 2
+    q, kc, vc, table = _cache(sum(kv) + d, kv, H, H // G, d, page, T, garbage=float("inf"))
+    lam, w = torch.tensor([0.3], device=DEV), torch.linspace(0.5, 1.5, 2 * d, device=DEV)
+    plan = api.extend_plan(i32(cu), i32(kv), T, H, H // G, d, max(new), causal)
+    out = torch.full((T, H, 2 * d), 5.0, device=DEV).bfloat16()
+    api.diffattn_extend(q, kc, vc, i32(table), plan, lam, 0.4, w, out=out)
+    _check_on_device(out, q, kc, vc, table, cu, kv, float(lam), w, causal)
+    assert (out[T - 2:] == 5.0).all()
+
+
+@pytest.mark.parametrize("seed", range(10))
+def test_step_random(seed):
+    r = np.random.default_rng(seed + 100)
+    case = _step_case(seed + 50, int(r.integers(1, 900)), int(r.choice([1, 3, 16, 24, 256])), int(r.integers(0, 4000)),
+                      int(r.integers(0, 400)), int(r.integers(0, 20)))
+    assert _check_step(case, case[6] + int(r.integers(0, 50)), bool(seed & 1))[3] == 0
+
+
+def test_debug_build_gives_the_same_bits():
+    from differential_attention_04_b200 import _lib
+    from differential_attention_04_b200.build import build
+    q, kc, vc, table, cu, plan, lam, w = _plain([1, 1, 3, 200, 40], [900, 4000, 700, 1500, 40], 6, 3, 128, 16)
+    pos, rot = i32(np.arange(q.shape[0])), api.rope_table(300, 128)
+    run = lambda: (api.diffattn_extend(q, kc, vc, i32(table), plan, lam, 0.4, w), api.rope(q, None, pos, rot)[0])
+    want = run()
+    build(debug=True)
+    _lib.use_debug_library(True)
+    try:
+        got = run()
+        assert api.device_status() == api.OK
+    finally:
+        _lib.use_debug_library(False)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 def test_extend_without_a_plan_of_its_sizes():
     q, kc, vc, table, cu, plan, lam, w = _plain([1, 140], [50, 300], 2, 2, 64, 16)
     out = torch.full((q.shape[0], 2, 128), 3.0, device=DEV).bfloat16()
