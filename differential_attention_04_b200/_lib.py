@@ -15,6 +15,7 @@ DEBUG_LIB_PATH = os.path.join(_HERE, "libdiffattn_debug.so")
 
 _handles = {}
 _active = LIB_PATH
+_marshal = None  # the compiled marshalling module, bound to the active library; False: it was not built
 
 # name -> (restype, argtypes); mirrors include/diffattn.h
 _c_int, _c_float, _c_size, _vp, _c_ll = ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_longlong
@@ -88,9 +89,32 @@ def _load(path: str) -> ctypes.CDLL:
     return _handles[path]
 
 
+def _bind_marshal(handle: ctypes.CDLL) -> None:
+    """Point the marshalling module (if it was built) at a library's entry points."""
+    global _marshal
+    try:
+        from . import _marshal as m
+    except ImportError:  # the Python binding marshals every call then
+        _marshal = False
+        return
+    m.bind(*(ctypes.cast(getattr(handle, "diffattn_" + n), ctypes.c_void_p).value
+             for n in ("paged_step", "rope", "kv_append", "extend")))
+    _marshal = m
+
+
+def marshal():
+    """The marshalling module of the active library, or False where it was not built."""
+    if _marshal is None:
+        lib()
+    return _marshal
+
+
 def lib() -> ctypes.CDLL:
     """Load (once) and return the active library with typed entry points."""
-    return _load(_active)
+    handle = _load(_active)
+    if _marshal is None:
+        _bind_marshal(handle)
+    return handle
 
 
 def use_debug_library(on: bool = True) -> None:
@@ -99,4 +123,4 @@ def use_debug_library(on: bool = True) -> None:
     The two are separate libraries, each with its own device status word."""
     global _active
     _active = DEBUG_LIB_PATH if on else LIB_PATH
-    _load(_active)
+    _bind_marshal(_load(_active))

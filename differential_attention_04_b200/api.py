@@ -3,6 +3,10 @@
 Argument marshalling only: every step of the computation runs in the CUDA
 library.  Tensors are passed by device pointer on the current torch stream;
 the functions return immediately (stream-ordered), like the C calls.
+
+The calls that a server makes every step are first offered to the compiled
+marshalling module (csrc/marshal.cpp): it makes the call when everything is
+plainly right, and otherwise the checks below say what is wrong.
 """
 from __future__ import annotations
 
@@ -11,7 +15,7 @@ from typing import NamedTuple
 
 import torch
 
-from ._lib import lib
+from ._lib import lib, marshal
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_WORKSPACE, ERR_BOUNDS = range(7)
 F32, BF16 = 0, 1
@@ -72,6 +76,13 @@ def _launch(name: str, tensors, *args) -> None:
             status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     if status != OK:
         raise DiffAttnError(name, status)
+
+
+def _made(name: str, status: int) -> bool:
+    """Whether the marshalling module made the call (its status: negative if it was left to the checks here)."""
+    if status > 0:
+        raise DiffAttnError(name, status)
+    return status == 0
 
 
 # Shape and dtype checks run before the device check, so that every tensor the
@@ -489,6 +500,14 @@ def paged_step(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torc
     updated; free_pages: int32 ring of free pages, updated; pool: int32 [2] (head, count), replaced in place unless
     pool_out is given; num_tokens: rows of positions and slots (-1 behind the last new token).  info: int32 [4]
     (tokens, pages taken, pages returned, 0 or what is wrong; then the step took nothing)."""
+    fast = marshal()
+    if fast and (out is None or len(out) == 5):
+        r = fast.paged_step(ctx_lens, new_lens, block_table, free_pages, pool, pool if pool_out is None else pool_out,
+                            page_size, num_tokens, *((None,) * 5 if out is None else out))
+        if type(r) is tuple:
+            return r
+        if _made("diffattn_paged_step", r):
+            return tuple(out)
     _need(ctx_lens.dim() == 1 and block_table.dim() == 2 and free_pages.dim() == 1,
           "ctx_lens must be [S], block_table [S, max_pages] and free_pages [ring_size]")
     S, max_pages = block_table.shape
@@ -547,6 +566,12 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table
     rope_table_scaled, whose width says how many channels are rotated.  Rows with a negative position are left as
     they are in `out` (which may be (q, k) itself).  ``inverse`` is the transposed map: gradients with respect to
     q', k' go in, those with respect to q, k come out."""
+    if out is None:
+        out = (torch.empty_like(q), None if k is None else torch.empty_like(k))
+    _need(len(out) == 2, "out must hold (q', k')")
+    fast = marshal()
+    if fast and _made("diffattn_rope", fast.rope(q, k, positions, table, layout, 1 if inverse else 0, *out)):
+        return tuple(out)
     qs = q.shape
     _need(len(qs) >= 4 and qs[-2] == 2, "q must be [..., H, 2, d]")
     H, d = qs[-3], qs[-1]
@@ -561,9 +586,6 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table
               "k must be [..., H_kv, 2, d] with q's rows and dtype")
         H_kv = ks[-3]
     n_pos, rot = _rope_args(d, positions, table, T)
-    if out is None:
-        out = (torch.empty_like(q), None if k is None else torch.empty_like(k))
-    _need(len(out) == 2, "out must hold (q', k')")
     qo, ko = out
     _same("q'", qo, qs, q.dtype)
     _need((ko is None) == (k is None), "out must hold k' exactly when k is given")
@@ -600,14 +622,18 @@ def kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torc
     """The cache write of a step: returns q rotated at `positions`, and writes k rotated and v into the pages at
     `slots` (int32 [T], page * page_size + offset; negative: nothing is written).  q: bfloat16 [T, H, 2, d];
     k: [T, H_kv, 2, d]; v: [T, H_kv, 2d]; table None: no rotation."""
+    if out is None:
+        out = torch.empty_like(q)
+    fast = marshal()
+    if fast and _made("diffattn_kv_append",
+                      fast.kv_append(q, k, v, positions, slots, table, k_cache, v_cache, layout, out)):
+        return out
     T, H, d = _rows(q)
     num_pages, page_size, H_kv = _cache_shapes(k_cache, v_cache, d, torch.bfloat16)
     _same("k", k, (T, H_kv, 2, d), torch.bfloat16)
     _same("v", v, (T, H_kv, 2 * d), torch.bfloat16)
     _i32("slots", slots, T)
     n_pos = rot = 0
-    if out is None:
-        out = torch.empty_like(q)
     _same("out", out, (T, H, 2, d), torch.bfloat16)
     ts = (q, k, v, slots, k_cache, v_cache, out)
     if table is not None:
@@ -658,6 +684,10 @@ def diffattn_extend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     """Differential attention of the step's new tokens over the paged cache.  q: bfloat16 [T, H, 2, d]; k_cache:
     [num_pages, page_size, H_kv, 2, d]; v_cache: [num_pages, page_size, H_kv, 2d]; block_table: int32
     [S, max_pages]; plan: extend_plan's.  Rows behind the last request are left as they are in `out`."""
+    fast = marshal()
+    if fast and workspace is not None and out is not None and _made("diffattn_extend", fast.extend(
+            q, k_cache, v_cache, block_table, *plan, lam, lambda_init, rms_w, eps, mode, workspace, out)):
+        return out
     T, H, d = _rows(q)
     num_pages, page_size, H_kv = _cache_shapes(k_cache, v_cache, d, q.dtype)
     _need((T, H, H_kv, d) == (plan.T, plan.H, plan.H_kv, plan.d), "the plan was made for other sizes")

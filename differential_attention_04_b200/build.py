@@ -7,17 +7,21 @@ register / shared-memory usage per kernel.  ``--debug`` builds the
 bounds-checked variant instead (``-DDIFFATTN_DEBUG``, objects in
 ``_build_debug/``, library ``libdiffattn_debug.so``): its kernels check every
 global index and tensor-map coordinate, skip an access out of range and
-record DIFFATTN_ERR_BOUNDS in the status word.
+record DIFFATTN_ERR_BOUNDS in the status word.  ``csrc/marshal.cpp`` becomes the
+Python module ``_marshal`` (g++, against torch's headers), which marshals the
+calls that a server makes every step.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -27,6 +31,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdiffattn.so")
 BUILD_DEBUG = os.path.join(ROOT, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libdiffattn_debug.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -44,6 +49,27 @@ def _needs_build(obj: str, src: str) -> bool:
         glob.glob(os.path.join(INCLUDE, "*.h"))
     t = os.path.getmtime(obj)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def build_marshal(force: bool = False) -> str:
+    """The marshalling module, in-tree; its torch symbols are those of the torch that imports it."""
+    src, header = os.path.join(CSRC, "marshal.cpp"), os.path.join(INCLUDE, "diffattn.h")
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    newest = max(os.path.getmtime(f) for f in (src, header, os.path.join(torch_dir, "version.py")))
+    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= newest:
+        return MARSHAL
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = MARSHAL + ".tmp"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", src, "-o", tmp, "-I", INCLUDE,
+           "-isystem", os.path.join(torch_dir, "include"), "-isystem", os.path.join(cuda, "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-L", os.path.join(torch_dir, "lib"),
+           "-lc10", "-ltorch_cpu", "-ltorch_python", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError(f"g++ failed on {src}")
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
 
 
 def build(verbose_ptxas: bool = False, force: bool = False, debug: bool = False) -> str:
@@ -79,6 +105,8 @@ def build(verbose_ptxas: bool = False, force: bool = False, debug: bool = False)
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(tmp, lib)
+    if not debug:
+        build_marshal(force)
     return lib
 
 

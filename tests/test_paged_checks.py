@@ -107,3 +107,27 @@ def test_binding_refusals():
     _rejects("other sizes", api.diffattn_extend, q[:3], kc, vc, i(2, 3), plan, lam, 0.5, w)
     _rejects("block_table", api.diffattn_extend, q, kc, vc, i(3, 3), plan, lam, 0.5, w)
     _rejects("rms_w", api.diffattn_extend, q, kc, vc, i(2, 3), plan, lam, 0.5, w[:64])
+
+
+def test_marshalling_module_leaves_what_is_not_plain(L):
+    """Whatever is not plainly right (here: tensors that are not on a GPU, wrong counts, other objects) is left to the
+    binding's checks: the module has done nothing and says so."""
+    m = _lib.marshal()
+    assert m
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    none = (None,) * 5
+    step = (i(2), i(2), i(2, 3), i(9), i(2), i(2), 16, 4)
+    q, k, v, tab = bf(4, 4, 2, 64), bf(4, 2, 2, 64), bf(4, 2, 128), torch.zeros(9, 32, 2)
+    kc, vc = bf(3, 16, 2, 2, 64), bf(3, 16, 2, 128)
+    plan = (torch.zeros(64, dtype=torch.uint8), 2, 4, 4, 2, 64, 4)
+    ext = (q, kc, vc, i(2, 3), *plan, torch.zeros(1), 0.5, torch.ones(128), 1e-5, 0, plan[0], bf(4, 4, 128))
+    for f, args in ((m.paged_step, step + none), (m.paged_step, step), (m.paged_step, (1,) * 13),
+                    (m.paged_step, step[:6] + ("16", 4) + none), (m.rope, (q, k, i(4), tab, 0, 0, q, k)),
+                    (m.rope, (q, None, i(4), tab, 0, 0, q, None)), (m.rope, (None,) * 8), (m.rope, ()),
+                    (m.kv_append, (q, k, v, i(4), i(4), tab, kc, vc, 0, q)), (m.kv_append, (None,) * 10),
+                    (m.extend, ext), (m.extend, (None,) * 18), (m.extend, ext[:-1]),
+                    (m.extend, ext[:5] + (2 ** 70,) + ext[6:])):
+        assert f(*args) == -1
+    with pytest.raises(TypeError):
+        m.bind(1, 2)

@@ -550,6 +550,47 @@ def test_step_random(seed):
     assert _check_step(case, case[6] + int(r.integers(0, 50)), bool(seed & 1))[3] == 0
 
 
+def test_binding_and_marshalling_module_make_the_same_calls(monkeypatch):
+    from differential_attention_04_b200 import _lib
+    assert _lib.marshal()
+    q, kc, vc, bt, cu, plan, lam, w = _plain([1, 5, 30], [40, 70, 30], 4, 2, 64, 16)
+    T = q.shape[0]
+    g = torch.Generator(device=DEV).manual_seed(8)
+    k, v = (torch.randn(T, 2, n, generator=g, device=DEV).bfloat16().view(T, 2, *s) for n, s in ((128, (2, 64)), (128, (128,))))
+    tab = api.rope_table(200, 32)
+    case = _step_case(77, 40, 16, 300, 20, 5)
+
+    def run():
+        ctx, new, table, ring, pool, page, n = case
+        dt, dr, dp, po = i32(table), i32(ring), i32(pool), i32([0, 0])
+        res = [*api.paged_step(i32(ctx), i32(new), dt, dr, dp, page, n + 3, pool_out=po), dt, dr, po]
+        out = tuple(torch.zeros_like(t) for t in res[:5])
+        dt2, dr2 = i32(table), i32(ring)
+        res += list(api.paged_step(i32(ctx), i32(new), dt2, dr2, dp, page, n + 3, out=out)) + [dp, dt2]
+        pos, slots = i32(np.arange(T)), i32(np.arange(T)[::-1].copy())
+        res += list(api.rope(q, k, pos, tab, api.ROPE_HALF, True)) + [api.rope(q.float(), None, pos, tab)[0]]
+        a, b = kc.clone(), vc.clone()
+        res += [api.kv_append(q, k, v, pos, slots, tab, a, b, api.ROPE_HALF), a, b]
+        a, b = kc.clone(), vc.clone()
+        res += [api.kv_append(q, k, v, None, slots, None, a, b), a, b]
+        ws = torch.empty(max(16, api.extend_workspace_size(plan)), dtype=torch.uint8, device=DEV)
+        out = torch.zeros(T, 4, 128, device=DEV).bfloat16()
+        return res + [api.diffattn_extend(q, kc, vc, i32(bt), plan, lam, 0.4, w, workspace=ws, out=out)]
+
+    fast = run()
+    # refusals by the library come through with their status, and the checks' with their messages
+    refuse = lambda: [pytest.raises(api.DiffAttnError, api.rope, q, None, i32(np.arange(T)), tab, 7).value.status,
+                      str(pytest.raises(ValueError, api.rope, q, None, i32(np.arange(T))[:-1], tab).value),
+                      str(pytest.raises(ValueError, api.kv_append, q, k, v.transpose(1, 2), i32(np.arange(T)),
+                                        i32(np.arange(T)), tab, kc, vc).value)]
+    said = refuse()
+    monkeypatch.setattr(_lib, "_marshal", False)
+    assert not _lib.marshal()
+    for x, y in zip(fast, run()):
+        assert torch.equal(x, y)
+    assert refuse() == said
+
+
 def test_debug_build_gives_the_same_bits():
     from differential_attention_04_b200 import _lib
     from differential_attention_04_b200.build import build
