@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
   // the workers: where each begins, and the item that it leaves unfinished
   for (int i = tid; i < kNarrowWorkers + wide_workers(n.d); i += kPlanThreads) {
     const int c = i >= kNarrowWorkers, w = c ? i - kNarrowWorkers : i;
-    WorkStart st{0, 0, 0, 0};
+    WorkStart st{};
     WorkTail tl{0, 0, 0, 0};
     if (w < W[c]) {
       const int ic = c ? wc : kNarrowCost;
@@ -281,7 +281,9 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
         const long long all = c ? wunits * n.H_kv : nunits;
         const long long u0 = x0.b + x0.unit, u1 = last || cut[c][w + 1] >= U[c] ? all : x1.b + x1.unit;
         auto index = [&](const Spot& x) { return c ? static_cast<int>(item_index(wide[x.at], x.at, x.hk)) : x.at; };
-        if (u1 > u0) st = WorkStart{index(x0), x0.hk, static_cast<int>(x0.unit), static_cast<int>(u1 - u0)};
+        if (u1 > u0)
+          st = WorkStart{index(x0), x0.hk, static_cast<int>(x0.unit), static_cast<int>(u1 - u0),
+                         c ? NarrowReq{} : narrow[x0.at]};
         // The item that the range ends in is split if the next worker begins
         // inside it.  Its owner is the last worker that begins at or before
         // its first unit.

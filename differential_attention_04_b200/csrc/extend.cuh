@@ -68,10 +68,11 @@ struct WideItem {
   int L, s, hk;    // cached tokens, request, key head
   int tile;        // in the schedule's list of row tiles
 };
-// Where a worker's range begins: item (list index, and key head of a narrow
-// one), its unit, and how many units it takes.
+// Where a worker's range begins: item (list index, and key head and request of
+// a narrow one), its unit, and how many units it takes.
 struct WorkStart {
   int at, hk, unit, count;
+  NarrowReq rq;
 };
 // The split item that the range ends in and that goes on behind it, in how
 // many parts (0: there is none), and which of them the worker has.

@@ -36,7 +36,7 @@
 // shared memory and the row is finished here, or its unnormalised sums go to a
 // record if the item is split.  The second CTA of an SM loads and computes
 // under the first one's merge: one CTA of four pairs took 141 us for 256
-// requests of 80 tokens over 16 heads where this takes 88, and 386 us for 24 x 5
+// requests of 80 tokens over 16 heads where this takes 80, and 386 us for 24 x 5
 // drafted tokens where this takes 355 (a lone request of 1000 tokens: 14 and 17
 // us).
 //
@@ -109,17 +109,15 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 struct Cursor {
   NarrowReq rq;
   int at, hk, unit, units;
-  __device__ void open(const NarrowReq* list) {
-    rq = list[at];
-    units = rq.L <= 0 ? 1 : (rq.L - 1) / kUnit + 1;
-  }
+  __device__ void count_units() { units = rq.L <= 0 ? 1 : (rq.L - 1) / kUnit + 1; }
+  __device__ explicit Cursor(const WorkStart& st) : rq(st.rq), at(st.at), hk(st.hk), unit(st.unit) { count_units(); }
   // The item behind this one (only called while the worker has units left).
   __device__ void next(const NarrowReq* list, int H_kv) {
     unit = 0;
     if (++hk == H_kv) {
       hk = 0;
-      ++at;
-      open(list);
+      rq = list[++at];
+      count_units();
     }
   }
 };
@@ -136,9 +134,9 @@ __global__ void __launch_bounds__(kThreads, 2) extend_narrow_kernel(const Extend
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kPairs][2][RT], s_l[kPairs][2][RT], s_ss[2 * kPairs][RT];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, pair = warp & (kPairs - 1), map = warp / kPairs;
-  if (!plan_fits(a.plan, a.n, status)) return;
   const PlanView pv = plan_view(a.plan, a.n, 0);
-  const WorkStart st = pv.starts[blockIdx.x];
+  const WorkStart st = pv.starts[blockIdx.x];  // read beside the header: the first loads are one chain of trips to L2
+  if (!plan_fits(a.plan, a.n, status)) return;
   if (st.count == 0) return;
   const int causal = pv.head->causal;
   const int H = a.n.H, H_kv = a.n.H_kv, G = H / H_kv;
@@ -148,11 +146,7 @@ __global__ void __launch_bounds__(kThreads, 2) extend_narrow_kernel(const Extend
   // ------------------------------------------------------------- the loads --
   const char* cache = static_cast<const char*>(map ? a.v_cache : a.k_cache);
   const uint32_t mine = ring + (map ? kSlice * C::ROW : 0);
-  Cursor ld{};
-  ld.at = st.at;
-  ld.hk = st.hk;
-  ld.unit = st.unit;
-  ld.open(pv.narrow);
+  Cursor ld(st);
   constexpr int SPU = kUnit / (kPairs * kSlice * SL);  // steps a unit
   // where step i's slice x of this pair begins in the unit
   auto slice_at = [&](int i, int x) { return ((i % SPU * SL + x) * kPairs + pair) * kSlice; };
@@ -193,11 +187,7 @@ __global__ void __launch_bounds__(kThreads, 2) extend_narrow_kernel(const Extend
   // ------------------------------------------------------------ the items --
   const float sc = kLog2e * rsqrtf(static_cast<float>(D));
   const float c2 = map2_coefficient(a.mode, *a.lambda);
-  Cursor cur{};
-  cur.at = st.at;
-  cur.hk = st.hk;
-  cur.unit = st.unit;
-  cur.open(pv.narrow);
+  Cursor cur(st);
   // the queries of an item as the operand of S^T (this map's)
   uint32_t qf[NT][KS][2];
   auto load_q = [&](const Cursor& it) {
