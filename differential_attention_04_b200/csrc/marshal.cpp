@@ -75,8 +75,8 @@ struct Args {
     ok = false;
     return nullptr;
   }
-  // Whether the call can be made: the tensors' device is the current one.
-  bool ready() const { return ok && device >= 0 && c10::cuda::current_device() == device; }
+  // Whether the call can be made: a library is bound, and the tensors' device is the current one.
+  bool ready() const { return ok && g_extend && device >= 0 && c10::cuda::current_device() == device; }
   cudaStream_t stream() const { return c10::cuda::getCurrentCUDAStream(device).stream(); }
 };
 
@@ -93,10 +93,19 @@ PyObject* guarded(F f) {
   }
 }
 
-#define WITHOUT_GIL(call)    \
-  int st;                    \
-  Py_BEGIN_ALLOW_THREADS st = (call); \
-  Py_END_ALLOW_THREADS
+// The interpreter is free while the library is called.  An object, so that an
+// exception from the arguments (a tensor without storage has no data_ptr) takes
+// the interpreter back on its way out.
+struct NoGil {
+  PyThreadState* state = PyEval_SaveThread();
+  ~NoGil() { PyEval_RestoreThread(state); }
+};
+#define WITHOUT_GIL(call) \
+  int st;                 \
+  {                       \
+    NoGil free;           \
+    st = (call);          \
+  }
 
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 4) {

@@ -591,6 +591,23 @@ def test_binding_and_marshalling_module_make_the_same_calls(monkeypatch):
     assert refuse() == said
 
 
+def test_binding_refuses_tensors_without_storage():
+    """A batched tensor of torch.vmap looks like any other until its address is asked for."""
+    pos, tab = i32([0, 1, 2, 3]), api.rope_table(8, 64, device=DEV)
+    kc, vc = torch.zeros(2, 16, 2, 2, 64, device=DEV).bfloat16(), torch.zeros(2, 16, 2, 128, device=DEV).bfloat16()
+    plan = api.extend_plan(i32([0, 4]), i32([4]), 4, 2, 2, 64, 4)
+    ws = torch.empty(api.extend_workspace_size(plan), dtype=torch.uint8, device=DEV)
+    lam, w, bt = torch.tensor([0.3], device=DEV), torch.ones(128, device=DEV), i32([[0]])
+    x, v = torch.randn(3, 4, 2, 2, 64, device=DEV).bfloat16(), torch.randn(3, 4, 2, 128, device=DEV).bfloat16()
+    lens = torch.ones(3, 1, dtype=torch.int32, device=DEV)
+    for f in (lambda a, b, n: api.rope(a, None, pos, tab)[0], lambda a, b, n: api.kv_append(a, a, b, pos, pos, tab, kc, vc),
+              lambda a, b, n: api.diffattn_extend(a, kc, vc, bt, plan, lam, 0.4, w, workspace=ws, out=b),
+              lambda a, b, n: api.paged_step(n, n, bt, i32([1]), i32([0, 1]), 16, 4)[0]):
+        with pytest.raises((RuntimeError, ValueError)):
+            torch.vmap(f)(x, v, lens)
+    assert not kc.any() and not vc.any()
+
+
 def test_debug_build_gives_the_same_bits():
     from differential_attention_04_b200 import _lib
     from differential_attention_04_b200.build import build
