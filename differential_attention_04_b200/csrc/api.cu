@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 
 #include "diffattn.h"
@@ -285,6 +286,27 @@ int check_rotation(int T, int H, int H_kv, int d, int rot, int layout, const voi
   if (!aligned16(table) || !aligned4(positions)) return DIFFATTN_ERR_INVALID_ARG;
   if (d % 8 || d > 256) return DIFFATTN_ERR_UNSUPPORTED;
   return DIFFATTN_OK;
+}
+
+// A buffer of a call; an absent one overlaps nothing.
+struct Span {
+  const void* p;
+  long long bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x && y && a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes;
+}
+// Whether a written buffer overlaps a read one or another written one.  Blocks
+// read and write in no order, so such a call would give what the order gives.
+bool overlaps(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  for (auto w = written.begin(); w != written.end(); ++w) {
+    for (const Span& r : read)
+      if (overlap(*w, r)) return true;
+    for (auto v = written.begin(); v != w; ++v)
+      if (overlap(*w, *v)) return true;
+  }
+  return false;
 }
 
 int check_extend_shape(const ExtendShape& n) {
@@ -621,6 +643,14 @@ int diffattn_rope(const void* q, const void* k, const int* positions, const floa
   if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || !aligned16(k_out)) return DIFFATTN_ERR_INVALID_ARG;
   if (!fits_i32(static_cast<long long>(T) * 2 * (H + H_kv) * d) || !fits_i32(static_cast<long long>(n_pos) * rot))
     return DIFFATTN_ERR_INVALID_ARG;
+  {
+    const long long row = 2LL * d * (dtype == DIFFATTN_BF16 ? 2 : 4);
+    const Span qo = {q_out, T * H * row}, ko = {H_kv ? k_out : nullptr, T * H_kv * row};
+    // an output may be its input
+    if (overlaps({qo, ko}, {{q == q_out ? nullptr : q, qo.bytes}, {H_kv && k != k_out ? k : nullptr, ko.bytes},
+                            {positions, 4LL * T}, {table, 4LL * n_pos * rot}}))
+      return DIFFATTN_ERR_INVALID_ARG;
+  }
   RopeParams p = {};
   p.q = q;
   p.k = k;
@@ -662,6 +692,13 @@ int diffattn_kv_append(const void* q, const void* k, const void* v, const int* p
   if (!fits_i32(static_cast<long long>(T) * 2 * (H + H_kv) * d) || !fits_i32(static_cast<long long>(n_pos) * rot) ||
       !fits_i32(static_cast<long long>(num_pages) * page_size))
     return DIFFATTN_ERR_INVALID_ARG;
+  {
+    const long long row = 4LL * d, kv = T * H_kv * row, pages = static_cast<long long>(num_pages) * page_size * H_kv * row;
+    if (overlaps({{q_out, T * H * row}, {k_cache, pages}, {v_cache, pages}},
+                 {{q == q_out ? nullptr : q, T * H * row}, {k, kv}, {v, kv}, {table ? positions : nullptr, 4LL * T},
+                  {slots, 4LL * T}, {table, 4LL * n_pos * rot}}))
+      return DIFFATTN_ERR_INVALID_ARG;
+  }
   RopeParams p = {};
   p.q = q;
   p.k = k;
@@ -698,6 +735,17 @@ int diffattn_paged_step(const int* ctx_lens, const int* new_lens, int S, int* bl
                         static_cast<const void*>(info)})
     if (!aligned4(a)) return DIFFATTN_ERR_INVALID_ARG;
   if (S > kPagedStepMaxRequests) return DIFFATTN_ERR_UNSUPPORTED;
+  {
+    const long long s = 4LL * S, t = 4LL * T;
+    // (pool_out may be pool)
+    if (overlaps({{block_table, s * max_pages}, {free_pages, 4LL * ring_size}, {pool_out, 8}, {cu_q, s + 4},
+                  {kv_lens, s}, {positions, t}, {slots, t}, {info, 16}},
+                 {{ctx_lens, s}, {new_lens, s}}) ||
+        overlaps({{block_table, s * max_pages}, {free_pages, 4LL * ring_size}, {cu_q, s + 4}, {kv_lens, s},
+                  {positions, t}, {slots, t}, {info, 16}},
+                 {{pool, 8}}))
+      return DIFFATTN_ERR_INVALID_ARG;
+  }
   return cuda_status(launch_paged_step(ctx_lens, new_lens, S, block_table, max_pages, free_pages, ring_size, pool,
                                        pool_out, page_size, T, cu_q, kv_lens, positions, slots, info, stream));
 }
@@ -719,6 +767,8 @@ int diffattn_extend_plan(const int* cu_q, const int* kv_lens, int S, int T, int 
   if (st != DIFFATTN_OK) return st;
   if (!cu_q || !kv_lens || !aligned4(cu_q) || !aligned4(kv_lens)) return DIFFATTN_ERR_INVALID_ARG;
   if (!plan || plan_bytes < extend_plan_bytes(n) || !aligned16(plan)) return DIFFATTN_ERR_WORKSPACE;
+  if (overlaps({{plan, static_cast<long long>(extend_plan_bytes(n))}}, {{cu_q, 4LL * S + 4}, {kv_lens, 4LL * S}}))
+    return DIFFATTN_ERR_INVALID_ARG;
   DevCtl ctl;
   if (dev_ctl(&ctl) != cudaSuccess) return DIFFATTN_ERR_CUDA;
   return cuda_status(launch_extend_plan(cu_q, kv_lens, n, causal, plan, ctl, stream));
@@ -744,6 +794,13 @@ int diffattn_extend(const void* q, const void* k_cache, const void* v_cache, con
   if (!plan || plan_bytes < extend_plan_bytes(a.n) || !aligned16(plan)) return DIFFATTN_ERR_WORKSPACE;
   const size_t need = extend_workspace_bytes(a.n);
   if (need > 0 && (!workspace || ws_bytes < need || !aligned16(workspace))) return DIFFATTN_ERR_WORKSPACE;
+  {
+    const long long row = 4LL * d, pages = static_cast<long long>(num_pages) * page_size * H_kv * row;
+    if (overlaps({{o, T * H * row}, {need > 0 ? workspace : nullptr, static_cast<long long>(need)}},
+                 {{q, T * H * row}, {k_cache, pages}, {v_cache, pages}, {block_table, 4LL * S * max_pages},
+                  {plan, static_cast<long long>(extend_plan_bytes(a.n))}, {lambda, 4}, {rms_w, 8LL * d}}))
+      return DIFFATTN_ERR_INVALID_ARG;
+  }
   a.q = q;
   a.k_cache = k_cache;
   a.v_cache = v_cache;

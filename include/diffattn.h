@@ -491,6 +491,8 @@ int diffattn_decode_noalloc(const void* q, const void* k_cache,
  *                pool_out is pool, and the other three values say what the
  *                step would have needed (at most 2^31 - 1).
  * S at most 8192 (DIFFATTN_ERR_UNSUPPORTED beyond); pointers 4-byte aligned.
+ * No buffer that is written may overlap another one (kv_lens not ctx_lens:
+ * DIFFATTN_ERR_INVALID_ARG), pool_out and pool excepted.
  */
 int diffattn_paged_step(const int* ctx_lens, const int* new_lens, int S, int* block_table, int max_pages,
                         int* free_pages, int ring_size, const int* pool, int* pool_out, int page_size, int T,
@@ -526,7 +528,7 @@ typedef enum {
  * diffattn_rope -- queries and keys rotated at given positions (after a
  * projection without a table; packed or padded batches; part of the head).
  *   q, q_out : [T, H, 2, d], k, k_out : [T, H_kv, 2, d], dtype F32 or BF16; the
- *              outputs may be the inputs (and no other overlap); H_kv = 0: no k
+ *              outputs may be the inputs (any other overlap is refused); H_kv = 0: no k
  *   positions: device int32[T]; a row with a negative position is padding and
  *              its output is left as it is
  *   table    : device float32 [n_pos][rot / 2][2], as the table calls write it
@@ -548,6 +550,7 @@ typedef enum {
  *   slots    : device int32[T]; a row with a negative slot writes no key or
  *              value; one >= num_pages * page_size records
  *              DIFFATTN_ERR_BOUNDS and writes none.  No slot may occur twice.
+ *              q, k and v may not lie in the caches.
  * Errors of the three: DIFFATTN_ERR_INVALID_ARG, DIFFATTN_ERR_UNSUPPORTED,
  * DIFFATTN_ERR_CUDA.
  */
@@ -579,6 +582,7 @@ int diffattn_kv_append(const void* q, const void* k, const void* v, const int* p
  *                 is 0), 16-byte aligned, needs no initialisation.  Calls that
  *                 overlap on the GPU (and graphs that are replayed at the same
  *                 time) must not share one.
+ *   o and workspace may not overlap another buffer (o not q).
  * diffattn_extend_plan -- writes the schedule of a step (>=
  *   diffattn_extend_plan_size bytes, 16-byte aligned) from cu_q and kv_lens
  *   (device, as diffattn_paged_step writes them).  max_new is a host bound of

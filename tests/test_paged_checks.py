@@ -71,6 +71,39 @@ def test_extend_refusals(L):
         assert ex(ws=nul) == WS and ex(wn=8) == WS
 
 
+def test_overlapping_buffers_are_refused(L):
+    """Every buffer has a megabyte (a plan or a workspace 256) of its own; one that is moved into another's is refused
+    before anything is launched."""
+    at = lambda i, off=0: ctypes.c_void_p((i + 1 << 28) + off)
+    step = lambda **m: L.diffattn_paged_step(*(m.get(n, at(i)) for i, n in enumerate(("ctx", "new"))), 2,
+                                             m.get("bt", at(2)), 3, m.get("ring", at(3)), 9, m.get("pool", at(4)),
+                                             m.get("po", at(5)), 16, 4,
+                                             *(m.get(n, at(6 + i)) for i, n in enumerate(("cu", "kv", "pos", "sl", "info"))),
+                                             nul)
+    for m in (dict(kv=at(0)), dict(kv=at(0, 4)), dict(cu=at(1, -8)), dict(bt=at(0)), dict(ring=at(2, 20)),
+              dict(po=at(0)), dict(sl=at(8)), dict(info=at(4)), dict(pos=at(1, 4)), dict(ctx=at(2, 20))):
+        assert step(**m) == INV, m
+    rope = lambda Hk=2, q=at(0), k=at(1), qo=at(4), ko=at(5), pos=at(2), tab=at(3): L.diffattn_rope(
+        q, k, pos, tab, 8, 4, 2, Hk, 64, 64, 1, 0, 0, qo, ko, nul)
+    # 4 rows x 2 heads x 2 x 64 bf16: 2048 bytes
+    for m in (dict(qo=at(0, 16)), dict(qo=at(0, -2032)), dict(ko=at(0)), dict(qo=at(1)), dict(ko=at(4)),
+              dict(ko=at(4, 2032)), dict(qo=at(2)), dict(ko=at(3, 16)), dict(Hk=0, qo=at(0, 16))):
+        assert rope(**m) == INV, m
+    app = lambda q=at(0), k=at(1), v=at(2), qo=at(6), kc=at(7), vc=at(8): L.diffattn_kv_append(
+        q, k, v, at(3), at(4), at(5), 8, 4, 2, 2, 64, 64, 0, 3, 16, qo, kc, vc, nul)
+    for m in (dict(qo=at(0, 16)), dict(k=at(7)), dict(v=at(8, 512)), dict(vc=at(7)), dict(qo=at(1)), dict(q=at(7, 16))):
+        assert app(**m) == INV, m
+    ext = lambda q=at(0), kc=at(1), vc=at(2), bt=at(3), plan=at(4), lam=at(5), w=at(6), o=at(7), ws=at(8): \
+        L.diffattn_extend(q, kc, vc, bt, 3, 5, 16, plan, 1 << 28, 2, 8, 4, 2, 64, 4, lam, 0.5, w, 1e-5, 0, o, ws,
+                          1 << 28, nul)
+    for m in (dict(o=at(0)), dict(o=at(0, 16)), dict(o=at(2)), dict(o=at(4)), dict(ws=at(4)), dict(ws=at(0)),
+              dict(ws=at(7)), dict(o=at(8, 64)), dict(lam=at(7)), dict(w=at(8, 16)), dict(bt=at(7))):
+        assert ext(**m) == INV, m
+    n = L.diffattn_extend_plan_size(2, 8, 4, 2, 64, 4)
+    for cu, kv in ((at(0), at(1)), (at(1), at(0, 16)), (at(1), at(0, n - 4))):
+        assert L.diffattn_extend_plan(cu, kv, 2, 8, 4, 2, 64, 4, 1, at(0), 1 << 28, nul) == INV
+
+
 def _rejects(match, fn, *a, **k):
     with pytest.raises(ValueError, match=match):
         fn(*a, **k)
