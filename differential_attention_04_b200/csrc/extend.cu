@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
     for (int v = 0; v < tid; ++v) used += whole_cost[v];
     cut[1][tid] = at + tid * U[1] / W[1] - used;
   }
-  if (tid == 0) *head = PlanHeader{{W[0], W[1]}, causal, ntiles, n, kPlanMagic, rounds, {}};
+  if (tid == 0) *head = PlanHeader{{W[0], W[1]}, causal, ntiles, n, kPlanMagic, rounds, {nunits, wunits}};
   __syncthreads();
   // the workers: where each begins, and the item that it leaves unfinished
   for (int i = tid; i < kNarrowWorkers + wide_workers(n.d); i += kPlanThreads) {
@@ -315,10 +315,10 @@ constexpr int kJoinWideBlocks = kWideRows / kJoinWarps;  // blocks of a wide wor
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) extend_join_kernel(const ExtendArgs a, const float* nrecs,
-                                                                   const float* wrecs, int* status) {
+                                                                   const float* wrecs, UnitLimits most, int* status) {
   constexpr int DV = 2 * D;
   constexpr int NV = 2 * DV / 128;  // float4 of a lane: first map 1's channels, then the same of map 2
-  if (!plan_fits(a.plan, a.n, status)) return;
+  if (!plan_fits(a.plan, a.n, most, status)) return;
   const bool is_wide = blockIdx.x >= kNarrowWorkers;
   const int bi = is_wide ? blockIdx.x - kNarrowWorkers : blockIdx.x;
   const int blocks = is_wide ? kJoinWideBlocks : 1;
@@ -512,11 +512,12 @@ cudaError_t launch_extend(const ExtendArgs& a, DevCtl ctl, cudaStream_t stream) 
   if (e != cudaSuccess) return e;
   // no item can be split where every request's keys fit one unit
   if (!wide && static_cast<long long>(a.max_pages) * a.page_size <= kUnit) return cudaSuccess;
+  const UnitLimits most = unit_limits(a.n, keys_of_table(a.max_pages, a.page_size));
   const unsigned grid = kNarrowWorkers + (wide ? wide_workers(a.n.d) * kJoinWideBlocks : 0);
   if (a.n.d == 128)
-    extend_join_kernel<128><<<grid, kJoinThreads, 0, stream>>>(a, nrecs, wrecs, ctl.status);
+    extend_join_kernel<128><<<grid, kJoinThreads, 0, stream>>>(a, nrecs, wrecs, most, ctl.status);
   else
-    extend_join_kernel<64><<<grid, kJoinThreads, 0, stream>>>(a, nrecs, wrecs, ctl.status);
+    extend_join_kernel<64><<<grid, kJoinThreads, 0, stream>>>(a, nrecs, wrecs, most, ctl.status);
   return cudaGetLastError();
 }
 

@@ -48,7 +48,7 @@ struct PlanHeader {
   ExtendShape shape;   // the sizes that the plan was made for
   int magic;
   int rounds;          // whole items of a wide worker
-  int pad[4];
+  long long units[2];  // of the narrow class, and of the wide class per key head
 };
 constexpr int kPlanMagic = 0x64706c6e;
 constexpr int kMaxKeys = 0x7fffff00;  // keys of a request: a unit behind the last one still has a 32-bit index
@@ -130,6 +130,12 @@ __host__ __device__ inline size_t record_floats(int rows, int d) {
   return static_cast<size_t>(rows) * (4 + 4 * d);
 }
 
+// The most keys of a request that a block table can hold.
+inline int keys_of_table(int max_pages, int page_size) {
+  const long long keys = static_cast<long long>(max_pages) * page_size;
+  return keys < kMaxKeys ? static_cast<int>(keys) : kMaxKeys;
+}
+
 struct PlanView {
   const PlanHeader* head;
   const WorkStart* starts;
@@ -137,12 +143,27 @@ struct PlanView {
   const NarrowReq* narrow;
   const WideItem* wide;
 };
-// Whether the buffer holds a plan of these sizes; the kernels do nothing otherwise.
-__device__ inline bool plan_fits(const void* plan, const ExtendShape& n, int* status) {
+// The most units that a call works off (PlanHeader::units): what the block table
+// can hold, and some more.  A length costs its time even where its keys do not
+// enter, and 64 uninitialised ones of 2^30 keys would take seconds.  Below the
+// limit a worker's units and steps fit 32 bits.
+struct UnitLimits {
+  long long units[2];
+};
+inline UnitLimits unit_limits(const ExtendShape& n, int max_keys) {
+  constexpr long long kSpare = 1 << 14, kMost = 1ll << 36;
+  const long long per = max_keys / kUnit + 1, narrow = (n.S * per + kSpare) * n.H_kv;
+  const long long wide = plan_layout(n).max_tiles * per + kSpare;
+  return UnitLimits{{narrow < kMost ? narrow : kMost, wide < kMost / n.H_kv ? wide : kMost / n.H_kv}};
+}
+// Whether the buffer holds a plan of these sizes within the limits; the kernels
+// do nothing otherwise.
+__device__ inline bool plan_fits(const void* plan, const ExtendShape& n, const UnitLimits& most, int* status) {
   const PlanHeader* h = static_cast<const PlanHeader*>(plan);
   const ExtendShape& p = h->shape;
   const bool ok = h->magic == kPlanMagic && p.S == n.S && p.T == n.T && p.H == n.H && p.H_kv == n.H_kv &&
-                  p.d == n.d && p.max_new == n.max_new;
+                  p.d == n.d && p.max_new == n.max_new &&
+                  h->units[0] <= most.units[0] && h->units[1] <= most.units[1];
   if (!ok) atomicCAS(status, 0, 6);
   return ok;
 }

@@ -128,7 +128,8 @@ struct Cursor {
 // says which; a kernel for 16 rows has no registers to spare).
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, 2) extend_narrow_kernel(const ExtendArgs a, float* recs, int page_shift,
-                                                                    int max_keys, int one_unit, int* status) {
+                                                                    int max_keys, int one_unit, UnitLimits most,
+                                                                    int* status) {
   using C = Narrow<D>;
   constexpr int DV = C::DV, KS = D / 16, CT = DV / 16, RT = 8 * NT, SL = C::SL;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 2) extend_narrow_kernel(const Extend
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, pair = warp & (kPairs - 1), map = warp / kPairs;
   const PlanView pv = plan_view(a.plan, a.n, 0);
   const WorkStart st = pv.starts[blockIdx.x];  // read beside the header: the first loads are one chain of trips to L2
-  if (!plan_fits(a.plan, a.n, status)) return;
+  if (!plan_fits(a.plan, a.n, most, status)) return;
   if (st.count == 0) return;
   const int causal = pv.head->causal;
   const int H = a.n.H, H_kv = a.n.H_kv, G = H / H_kv;
@@ -493,9 +494,9 @@ cudaError_t launch_d(const ExtendArgs& a, float* recs, DevCtl ctl, cudaStream_t 
   int shift = 0;
   while ((1 << shift) < a.page_size) ++shift;
   const long long keys = static_cast<long long>(a.max_pages) * a.page_size;
-  const int max_keys = keys < kMaxKeys ? static_cast<int>(keys) : kMaxKeys;
+  const int max_keys = keys_of_table(a.max_pages, a.page_size);
   extend_narrow_kernel<D, NT><<<kNarrowWorkers, kThreads, Narrow<D>::SMEM, stream>>>(
-      a, recs, shift, max_keys, keys <= kUnit && !wide_possible(a.n), ctl.status);
+      a, recs, shift, max_keys, keys <= kUnit && !wide_possible(a.n), unit_limits(a.n, max_keys), ctl.status);
   return cudaGetLastError();
 }
 }  // namespace

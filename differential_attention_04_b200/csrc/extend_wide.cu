@@ -87,7 +87,7 @@ static_assert(sizeof(Bars) <= 256, "barriers");
 __global__ void __launch_bounds__(kThreads, 1)
     extend_wide_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const WideParams p) {
-  if (!plan_fits(p.plan, p.n, p.status)) return;  // the same for both CTAs of the cluster
+  if (!plan_fits(p.plan, p.n, p.most, p.status)) return;  // the same for both CTAs of the cluster
   const PlanView pv = plan_view(p.plan, p.n, 1);
   Walk wk;
   if (!wk.begin(pv, blockIdx.x >> 1)) return;  // and this too
@@ -568,8 +568,8 @@ WideParams wide_params(const ExtendArgs& a, float* recs, DevCtl ctl) {
   p.max_pages = a.max_pages;
   p.num_pages = a.num_pages;
   while ((1 << p.page_shift) < a.page_size) ++p.page_shift;
-  const long long keys = static_cast<long long>(a.max_pages) * a.page_size;
-  p.max_keys = keys < kMaxKeys ? static_cast<int>(keys) : kMaxKeys;
+  p.max_keys = keys_of_table(a.max_pages, a.page_size);
+  p.most = unit_limits(a.n, p.max_keys);
   p.o = static_cast<__nv_bfloat16*>(a.o);
   p.recs = recs;
   p.lambda = a.lambda;

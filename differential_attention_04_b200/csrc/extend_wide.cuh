@@ -19,6 +19,7 @@ struct WideParams {
   ExtendShape n;
   const int* block_table;
   int max_pages, num_pages, page_shift, max_keys;
+  UnitLimits most;
   __nv_bfloat16* o;
   float* recs;
   const float* lambda;

@@ -86,7 +86,7 @@ static_assert(sizeof(Bars) <= 256, "barriers");
 __global__ void __launch_bounds__(kThreads, 1)
     extend_wide64_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                          const __grid_constant__ CUtensorMap tv, const WideParams p) {
-  if (!plan_fits(p.plan, p.n, p.status)) return;
+  if (!plan_fits(p.plan, p.n, p.most, p.status)) return;
   const PlanView pv = plan_view(p.plan, p.n, 1);
   Walk wk;
   if (!wk.begin(pv, blockIdx.x)) return;

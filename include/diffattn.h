@@ -591,7 +591,9 @@ int diffattn_kv_append(const void* q, const void* k, const void* v, const int* p
  * than max_new new tokens, a negative length) records DIFFATTN_ERR_BOUNDS and
  * its rows are left as they are.  Pages are checked against num_pages: one out
  * of range records DIFFATTN_ERR_BOUNDS and reads as zeros.  Keys from
- * max_pages * page_size on record it too and do not enter.  Cached keys and
+ * max_pages * page_size on record it too and do not enter; where the lengths
+ * are together 2^21 keys and more beyond what the table can hold, nothing is
+ * computed (their time would be spent all the same).  Cached keys and
  * values behind kv_lens, whatever they hold, do not enter the result; those
  * before it must be finite (one that a query may not see enters with weight
  * zero).  A plan of other sizes, or none, records DIFFATTN_ERR_BOUNDS and

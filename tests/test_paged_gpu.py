@@ -391,6 +391,21 @@ def test_extend_table_too_narrow(new, kv):
     _check(out, q, kc, vc, table, cu, kv, float(lam), w)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("S,n,L", [(64, 1, 2 ** 30), (1, 1, 2 ** 31 - 257), (1, 140, 2 ** 31 - 257), (9, 40, 2 ** 27)])
+def test_extend_lengths_far_beyond_the_table(S, n, L, d):
+    """Lengths that no table of the call could hold are reported, at once and with nothing computed."""
+    q, kc, vc, table, cu, _, lam, w = _plain([n] * S, [200] * S, 4, 2, d, 16)
+    plan = api.extend_plan(i32(cu), i32([L] * S), S * n, 4, 2, d, n)
+    out = torch.full((S * n, 4, 2 * d), 3.0, device=DEV).bfloat16()
+    e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    e0.record()
+    api.diffattn_extend(q, kc, vc, i32(table), plan, lam, 0.4, w, out=out)
+    e1.record()
+    assert api.device_status() == api.ERR_BOUNDS
+    assert (out == 3.0).all() and e0.elapsed_time(e1) < 50
+
+
 def test_extend_plan_of_bad_offsets():
     """Requests whose entries do not fit are left out, and say so; the others are computed."""
     kv = [40, 60, 30]
