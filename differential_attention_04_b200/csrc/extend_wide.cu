@@ -36,7 +36,7 @@
 // item for its exchange and refill, which short prompts feel (74 x 128 tokens
 // over 12 heads: 147 us).  Measured: 2048 tokens behind 30K cached ones over 12
 // heads 906 us at full clock (1290 TFLOP/s), 1083 us in a loop under the power
-// cap; 2048 behind 6K 244 us.  Two softmax warpgroups with 64 keys each were
+// cap; 2048 behind 6K 237 us (239 without the pairs of F2).  Two softmax warpgroups with 64 keys each were
 // not faster here (chunk 1285 against 1280 us, mixed step 136 against 132).
 #include "extend_wide.cuh"
 
@@ -381,27 +381,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         float lsum = 0.f, t_mx = -INFINITY;
         auto make_p = [&](bool with_max) {
           const float mneg = m_run == -INFINITY ? 0.f : -m_run;
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
-          float mk[8];
+          const F2 sc2(sc, sc), mneg2(mneg, mneg);
+          F2 acc[2] = {F2(0.f, 0.f), F2(0.f, 0.f)};
+          float mk[4];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) mk[c] = -INFINITY;
+          for (int c = 0; c < 4; ++c) mk[c] = -INFINITY;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             uint32_t pk[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const float a0 = x[64 * half + 2 * i], a1 = x[64 * half + 2 * i + 1];
-              if (with_max) mk[i & 7] = fmaxf(mk[i & 7], fmaxf(a0, a1));
-              const float p0 = fast_exp2(fmaf(a0, sc, mneg));
-              const float p1 = fast_exp2(fmaf(a1, sc, mneg));
-              acc[i & 3] += p0 + p1;
+              if (with_max) mk[i & 3] = fmaxf(mk[i & 3], fmaxf(a0, a1));
+              float p0, p1;
+              fma2(F2(a0, a1), sc2, mneg2).get(p0, p1);
+              p0 = fast_exp2(p0);
+              p1 = fast_exp2(p1);
+              acc[i & 1] = add2(acc[i & 1], F2(p0, p1));
               pk[i] = pack_bf16x2(p0, p1);
             }
             tmem_st32(tl + C::TM_P + 64 * bb + 32 * half, pk);
           }
-          lsum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-          if (with_max)
-            t_mx = fmaxf(fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])), fmaxf(fmaxf(mk[4], mk[5]), fmaxf(mk[6], mk[7]))) * sc;
+          float l0, l1;
+          add2(acc[0], acc[1]).get(l0, l1);
+          lsum = l0 + l1;
+          if (with_max) t_mx = fmaxf(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3])) * sc;
         };
         make_p(true);
         // A jump of the maximum by more than 2^64 would overflow P: rescale O

@@ -31,6 +31,22 @@ struct WideParams {
   unsigned long long limit_ns;
 };
 
+// Two float32 in one register pair: Blackwell's packed instructions take the
+// pair in one issue slot.
+struct F2 {
+  uint64_t v;
+  __device__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ F2 fma2(F2 a, const F2& b, const F2& c) {
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a.v) : "l"(b.v), "l"(c.v));
+  return a;
+}
+__device__ __forceinline__ F2 add2(F2 a, const F2& b) {
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+  return a;
+}
+
 // A worker's walk over its segments: units unit .. unit + take - 1 of an item,
 // first its whole items (every workers-th up to `whole_end`), then its range of
 // the line.
