@@ -37,9 +37,10 @@
 // many of products (S at N = 64 costs 70 cycles an instruction, 35 of them
 // work), and the hand-overs between them.  Scores are scaled and weights added
 // in pairs (F2), and the maximum is formed in four chains: 223 us against 236
-// with single ones and eight chains (pairs alone 229).  A polynomial in place
-// of an eighth of the exponentials takes 227.  Measured: 808 TFLOP/s for 2048
-// tokens behind 6K over 16 heads (223 us).
+// with single ones and eight chains (pairs alone 229); one vote a tile instead
+// of two: 219.  A polynomial in place of an eighth of the exponentials takes
+// 2% more.  Measured: 823 TFLOP/s for 2048 tokens behind 6K over 16 heads (219
+// us).
 #include "extend_wide.cuh"
 
 namespace diffattn {
@@ -371,8 +372,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         make_p(true);
         // A jump of the maximum by more than 2^64 would overflow P: rescale O
         // to the new maximum (after the previous PV has completed) and redo P.
+        // (`grown`: one vote a tile where the maximum has hardly grown, the usual case)
+        const bool grown = __any_sync(0xffffffffu, t_mx > m_run + kRescaleThreshold);
         const bool hard = t > 0 && t_mx > m_run + kOverflowGuard;
-        if (__any_sync(0xffffffffu, hard)) {
+        if (grown && __any_sync(0xffffffffu, hard)) {
           tmem_st_wait();
           if (!(sm_ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[map][(g - 1) & 1], ((g - 1) >> 1) & 1, wc)))) break;
           tc_fence_after();
@@ -388,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Lazy rescale: keep the reference within 2^8 of the running maximum.
         // O is rescaled once this PV (which used the old reference) has completed.
         const bool need = t_mx > m_run + kRescaleThreshold;
-        if (__any_sync(0xffffffffu, need)) {
+        if (grown && __any_sync(0xffffffffu, need)) {
           if (!(sm_ok = __all_sync(0xffffffffu, mbar_wait(&bars->pv_done[map][b], (g >> 1) & 1, wc)))) break;
           tc_fence_after();
           rescale_o(need ? fast_exp2(m_run - t_mx) : 1.0f);
