@@ -35,7 +35,7 @@
 // chunks; memory for few rows over many keys; and about 20 thousand cycles an
 // item for its exchange and refill, which short prompts feel (74 x 128 tokens
 // over 12 heads: 147 us).  Measured: 2048 tokens behind 30K cached ones over 12
-// heads 906 us at full clock (1290 TFLOP/s), 1083 us in a loop under the power
+// heads 906 us at full clock (1290 TFLOP/s), 1030 us in a loop under the power
 // cap; 2048 behind 6K 237 us (239 without the pairs of F2).  Two softmax warpgroups with 64 keys each were
 // not faster here (chunk 1285 against 1280 us, mixed step 136 against 132).
 #include "extend_wide.cuh"
