@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ---------------------------------------------------- Q / K producer --
-    int gk = 0;  // K tiles issued
+    int gk = 0, gq = 0;  // K tiles and Q tiles issued
     bool ok = true;
     for (int k = 0; ok; ++k) {
       const int L = min(wk.t.L, p.max_keys);
@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_4d(sQ + blk * C::BLK_BYTES, &tq, &bars->q_full, blk * 64, static_cast<int>(rank), wk.t.hk * G,
                       wk.t.tok0);
       }
+      ++gq;
       for (int j = 0; j < wk.take; ++j, ++gk) {
         const int st = gk & 1, key0 = (wk.unit + j) * kBN;
         const int boxes = box.count(key0, L), row = box.row(p, wk.t, key0, boxes, lane);
@@ -186,7 +187,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok || !wk.next(pv)) break;
     }
-    // nothing may still be landing in shared memory when the CTA exits
+    // nothing may still be landing in shared memory when the CTA exits (after an
+    // abort no product may have waited for the last Q either)
+    mbar_wait(&bars->q_full, (gq - 1) & 1, wdrain);
     for (int j = max(0, gk - 2); j < gk; ++j) mbar_wait(&bars->k_full[j & 1], (j >> 1) & 1, wdrain);
     __syncwarp();
   } else if (warp == 2) {

@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ---------------------------------------------------- Q / K producer --
     if (lane == 0) {
-      int gk = 0;  // K tiles issued (all items)
+      int gk = 0, gq = 0;  // K tiles and Q tiles issued (all items)
       bool ok = true;
       for (int k = 0; ok; ++k) {
         const int idx = item_of(k);
@@ -276,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           mbar_arrive(&bars->q_full);
         }
+        ++gq;
         for (int j = 0; j < it.n_kv; ++j, ++gk) {
           const int st = gk & 1;
           if (!(ok = mbar_wait(&bars->k_empty[st], ((gk >> 1) & 1) ^ 1, wc))) break;
@@ -290,7 +291,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // nothing may still be landing in shared memory when the CTA exits
+      // nothing may still be landing in shared memory when the CTA exits (after
+      // an abort no product may have waited for the last Q either)
+      if (gq > 0) mbar_wait(&bars->q_full, (gq - 1) & 1, wdrain);
       for (int j = max(0, gk - 2); j < gk; ++j) mbar_wait(&bars->k_full[j & 1], (j >> 1) & 1, wdrain);
     }
     __syncwarp();
