@@ -316,15 +316,15 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     float4 rs = make_float4(0.f, 0.f, 0.f, 0.f);  // dQ: this query row's statistics
     if (KIND == kGradQ && grow < N) rs = p.stats[static_cast<size_t>(bh) * p.n_pad + grow];
     const float4* stv = reinterpret_cast<const float4*>(sST);
-    bool ok = true;
     for (int t = 0; t < T; ++t) {
       const int st = t % C::STAGES;
       const int sb = (C::NSB == 2) ? (t & 1) : 0;
       const uint32_t sph = (C::NSB == 2) ? ((t >> 1) & 1) : (t & 1);
-      if (!(ok = mbar_wait(&bars->s_full[sb], sph, wc))) break;
-      if constexpr (C::COL_STATS) {  // the stage's statistics (bulk copy) are visible after this wait
-        if (!(ok = mbar_wait(&bars->c_full[st], (t / C::STAGES) & 1, wc))) break;
-      }
+      // the warp leaves as one: after an abort a wait may end differently in its lanes
+      bool ok = mbar_wait(&bars->s_full[sb], sph, wc);
+      if constexpr (C::COL_STATS)  // the stage's statistics (bulk copy) are visible after this wait
+        ok = ok && mbar_wait(&bars->c_full[st], (t / C::STAGES) & 1, wc);
+      if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const uint32_t tb = tl + C::s_buf(t);
       uint32_t s1[NC], s2[NC], dp[C::HAS_DP ? NC : 1];

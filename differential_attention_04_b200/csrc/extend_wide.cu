@@ -442,7 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // ------------------------------------------------------ epilogue --
       // O is complete once the segment's last PV (and with it every earlier MMA) has.
-      if (sm_ok) sm_ok = mbar_wait(&bars->p_empty[(g - 1) & 1], ((g - 1) >> 1) & 1, wc);
+      // (A vote, as at every wait: its lanes may see it end differently after an abort.)
+      if (sm_ok) sm_ok = __all_sync(0xffffffffu, mbar_wait(&bars->p_empty[(g - 1) & 1], ((g - 1) >> 1) & 1, wc));
       tc_fence_after();
       if (!wk.whole()) {
         // a part of the row's keys: this map's sums to the worker's record

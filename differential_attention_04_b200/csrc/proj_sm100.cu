@@ -179,7 +179,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const int ab = lt & 1;
       int tm, tn;
       tile_coords(t, tm, tn);
-      if (!mbar_wait(&bars->acc_full[ab], (lt >> 1) & 1, wc)) break;
+      // the warp leaves as one: after an abort a wait may end differently in its lanes
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->acc_full[ab], (lt >> 1) & 1, wc))) break;
       tc_fence_after();
       const int m = tm * k2BM + 128 * static_cast<int>(rank) + r;
       const bool live = m < p.M;

@@ -74,3 +74,10 @@ def _aborts(run, limits=LIMITS, repeats=2):
 def test_split_rows(d, new, kv):
     run, plan = _call(new, kv, 3, 3, d, 16)
     _aborts(run)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_limits_that_run_out_anywhere(d):
+    """A wait may end in some lanes of a warp and run out in others: the warp has to leave as one."""
+    run, plan = _call([130], [6000], 2, 2, d, 64)
+    _aborts(run, range(150, 9000, 150), 1)
