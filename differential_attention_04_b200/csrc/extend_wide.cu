@@ -79,6 +79,7 @@ struct Bars {
   uint64_t p_full[2], p_empty[2];
   uint64_t mma_done;
   uint64_t exch_full, peer_ready, ss_full, epi_free;
+  uint64_t tile_full;  // per combined segment: its output tile is staged
   uint32_t tmem_base;
   volatile int abort;
 };
@@ -124,6 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars->peer_ready, 1);
     mbar_init(&bars->ss_full, 1);
     mbar_init(&bars->epi_free, 1);
+    mbar_init(&bars->tile_full, 4);  // one arrival per softmax warp
     bars->abort = 0;
     fence_mbarrier_init();
   }
@@ -287,9 +289,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     // stage 1), copy its rows out and free both V stages for the next segment.
     const uint32_t tile = smem_u32(sV + C::V_BYTES);
     const int own0 = (rank == 0) ? 0 : C::HALF;
+    int kt = 0;                    // tiles copied
+    unsigned long long tiles = 2;  // of keys since the last one, and the epilogue's share
     do {
+      tiles += wk.take;
       if (!wk.whole()) continue;
-      named_bar_sync(2, 160);  // with the softmax warps' arrivals
+      // The keys before a tile may take longer than one wait may: each of their
+      // tiles has the limit for itself, so this wait has it as often.
+      const WaitCtl wt{p.status, &bars->abort, __umul64hi(p.limit_ns, tiles) ? ~0ull : p.limit_ns * tiles};
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->tile_full, kt & 1, wt))) break;
+      ++kt;
+      tiles = 2;
       const int rows = wk.t.ntok * G, chunk = lane & 7;
 #pragma unroll
       for (int blk = 0; blk < C::HALF / 64; ++blk) {
@@ -445,6 +455,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (A vote, as at every wait: its lanes may see it end differently after an abort.)
       if (sm_ok) sm_ok = __all_sync(0xffffffffu, mbar_wait(&bars->p_empty[(g - 1) & 1], ((g - 1) >> 1) & 1, wc));
       tc_fence_after();
+      // After an abort nothing is exchanged, recorded or handed over any more:
+      // the four warps leave the walk together, and warp 3 by itself.
+      if (named_bar_or(1, 128, !sm_ok || bars->abort)) break;
       if (!wk.whole()) {
         // a part of the row's keys: this map's sums to the worker's record
         float* rec = p.recs + (2 * (blockIdx.x >> 1) + (wk.begins() ? 1 : 0)) * record_floats(kBM, D);
@@ -465,13 +478,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_bar_sync(1, 128);  // every row's tensor-memory reads are done
         if (tid == 128) mbar_arrive(&bars->epi_free);  // the next segment's first PV may overwrite O
         __syncwarp();
-        continue;
-      }
-      // After an abort nothing is exchanged any more (the waits for a partner
-      // that is gone would each run out); the four warps decide alike.
-      if (named_bar_or(1, 128, !sm_ok || bars->abort)) {
-        sm_ok = false;
-        named_bar_arrive(2, 160);
         continue;
       }
       // Both V stages are free of this segment's PV products: announce that
@@ -498,14 +504,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();  // the staged rows are read by the bulk copy (async proxy)
       __syncwarp();
       // the partner's receive buffer must be free before this CTA writes into it
-      const bool peer_ok = mbar_wait_acq_cluster(&bars->peer_ready, ke & 1, wc);
+      const bool peer_ok = __all_sync(0xffffffffu, mbar_wait_acq_cluster(&bars->peer_ready, ke & 1, wc));
       if (lane == 0 && peer_ok) {
         const int off = quarter * 32 * HALF;  // this warp's 32 rows, contiguous
         bulk_copy_s2cluster(map_to_cta(smem_u32(recv + off), partner), stage + off, 32 * HALF * 4,
                             map_to_cta(smem_u32(&bars->exch_full), partner));
         bulk_commit_group();
       }
-      mbar_wait(&bars->exch_full, ke & 1, wdrain);  // the partner's half has landed (even after an abort)
+      // the partner's half has landed (waited for even after an abort: a copy may be on its way)
+      const bool got_half = mbar_wait(&bars->exch_full, ke & 1, wdrain);
       float y[HALF];
       float ss = 0.f;
       const float* rrow = recv + r * HALF;
@@ -534,7 +541,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0 && peer_ok) bulk_wait_group_read0();  // the outgoing copy has left the staging rows
       __syncwarp();
       named_bar_sync(1, 128);  // every warp's outgoing copy is done with the rows the output tile reuses
-      mbar_wait_acq_cluster(&bars->ss_full, ke & 1, wdrain);
+      // a partner that is gone sends nothing: this CTA leaves at the next vote, before its barriers are armed again
+      if (!mbar_wait_acq_cluster(&bars->ss_full, ke & 1, wdrain) || !got_half) bars->abort = 1;
       const float rs = rsqrtf((ss + ssx[r]) / static_cast<float>(C::DV) + p.eps);
       const float gsc = (1.0f - p.lambda_init) * rs;
       // bf16 tile [64-column block][128 rows][64 columns], 128-byte swizzle, in the staging stage
@@ -552,8 +560,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++ke;
       // hand the staged tile to warp 3, which copies it out and frees the V
-      // stages, and go on with the next segment
-      named_bar_arrive(2, 160);
+      // stages, and go on with the next segment.  (An mbarrier, which waits with
+      // a limit and counts an arrival a phase: on a named barrier, warps that
+      // went through aborted segments could arrive twice before warp 3 did once,
+      // complete the barrier without it and leave it waiting for good.)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->tile_full);
     } while (wk.next(pv));
   }
 

@@ -81,3 +81,15 @@ def test_limits_that_run_out_anywhere(d):
     """A wait may end in some lanes of a warp and run out in others: the warp has to leave as one."""
     run, plan = _call([130], [6000], 2, 2, d, 64)
     _aborts(run, range(150, 9000, 150), 1)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,kv,limits", [([128] * 60, [128] * 60, (1, 2000, 10000, 40000)),
+                                           ([100, 256, 7] * 20, [260, 700, 90] * 20, (1, 5000, 20000))])
+def test_several_whole_items_a_worker(d, new, kv, limits):
+    """Items that are combined, exchanged between two blocks (d 128) and handed over one behind the other: a worker
+    that gives up has several of them left."""
+    run, plan = _call(new, kv, 16, 16, d, 64)
+    head = plan.buf[:64].view(torch.int32).tolist()
+    assert head[1] == (148 if d == 64 else 74) and head[11] >= 3, head  # workers, and the whole items of each
+    _aborts(run, limits)
