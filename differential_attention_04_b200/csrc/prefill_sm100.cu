@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ---------------------------------------------------- Q / K producer --
     if (lane == 0) {
-      int gk = 0, gq = 0;  // K tiles and Q tiles issued (all items)
+      int gk = 0;  // K tiles issued (all items)
       bool ok = true;
       for (int k = 0; ok; ++k) {
         const int idx = item_of(k);
@@ -276,7 +276,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           mbar_arrive(&bars->q_full);
         }
-        ++gq;
         for (int j = 0; j < it.n_kv; ++j, ++gk) {
           const int st = gk & 1;
           if (!(ok = mbar_wait(&bars->k_empty[st], ((gk >> 1) & 1) ^ 1, wc))) break;
@@ -291,9 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // nothing may still be landing in shared memory when the CTA exits (after
-      // an abort no product may have waited for the last Q either)
-      if (gq > 0) mbar_wait(&bars->q_full, (gq - 1) & 1, wdrain);
+      // nothing may still be landing in shared memory when the CTA exits
       for (int j = max(0, gk - 2); j < gk; ++j) mbar_wait(&bars->k_full[j & 1], (j >> 1) & 1, wdrain);
     }
     __syncwarp();
@@ -559,8 +556,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // ------------------------------------------------------ epilogue --
       // O is complete once the item's last PV (and with it every earlier MMA) has.
-      // (A vote, as at every wait: its lanes may see it end differently after an abort.)
-      if (sm_ok) sm_ok = __all_sync(0xffffffffu, mbar_wait(&bars->p_empty[(g - 1) & 1], ((g - 1) >> 1) & 1, wc));
+      // (How the wait ended is left alone: its lanes may see that differently
+      // after an abort, and sm_ok must not differ within a warp.  The next
+      // item's first wait, which is voted on, ends the work then.)
+      if (sm_ok) mbar_wait(&bars->p_empty[(g - 1) & 1], ((g - 1) >> 1) & 1, wc);
       tc_fence_after();
       if constexpr (OUT != kOutNorm) {
         // This map's O_i / l_i for the row, and lse_i = m + log2(l) in the
@@ -677,6 +676,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  // After an abort no product may have waited for the query tile that was
+  // issued last, and it must not be landing when the CTA exits.  Of the
+  // barrier's two phases one is behind and the other is that load's, or nobody's
+  // (which costs the limit, 10 ms).  Here and not at the end of the loads, with
+  // a count: any code before the softmax loop moves it, and 1% of the time with it.
+  if (tid == 0 && bars->abort) {
+    const WaitCtl wq{p.status, &drain_abort, 10000000ull};
+    mbar_wait(&bars->q_full, 0, wq);
+    mbar_wait(&bars->q_full, 1, wq);
+  }
+  __syncwarp();
   cluster_sync_all();  // no remote access to either CTA remains
   if (warp == 1) {
     tc_fence_after();
