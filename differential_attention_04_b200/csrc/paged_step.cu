@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(kStepThreads) paged_step_kernel(const StepPara
   const int status = s_bad;
   const bool ok = status == 0;
   const int total = ok ? static_cast<int>(carry.tok) : 0;
-  const int gtid = blockIdx.x * kStepThreads + tid, gsize = gridDim.x * kStepThreads;
+  // unsigned: tokens and pages may number 2^31 - 1, and an index takes one more step than there are
+  const unsigned gtid = blockIdx.x * kStepThreads + tid, gsize = gridDim.x * kStepThreads;
 
   if (gtid == 0) {
     p.info[0] = static_cast<int>(min(carry.tok, 0x7fffffffll));
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kStepThreads) paged_step_kernel(const StepPara
     }
   }
   // the requests' offsets and lengths
-  for (int s = gtid; s <= p.S; s += gsize) {
+  for (int s = static_cast<int>(gtid); s <= p.S; s += static_cast<int>(gsize)) {
     p.cu_q[s] = ok ? tok0[s] : 0;
     if (s < p.S) {
       const int n = p.nlen[s];
@@ -181,25 +182,25 @@ __global__ void __launch_bounds__(kStepThreads) paged_step_kernel(const StepPara
   // warp that walked its row alone would take a trip to memory per 32 of them
   // (14.7 us against 6.5 us in all for 700 requests of up to 32K tokens)
   if (ok) {
-    const int taken = static_cast<int>(carry.need), back = static_cast<int>(carry.rel);
-    for (int e = gtid; e < back; e += gsize) {
-      const int s = owner(rel0, e);
+    const unsigned taken = static_cast<unsigned>(carry.need), back = static_cast<unsigned>(carry.rel);
+    for (unsigned e = gtid; e < back; e += gsize) {
+      const int s = owner(rel0, static_cast<int>(e));
       p.ring[in_ring(static_cast<unsigned>(head) + count + e, p.F)] =
           p.bt[static_cast<size_t>(s) * p.max_pages + (e - rel0[s])];
     }
-    for (int e = gtid; e < taken; e += gsize) {
-      const int s = owner(need0, e);
+    for (unsigned e = gtid; e < taken; e += gsize) {
+      const int s = owner(need0, static_cast<int>(e));
       p.bt[static_cast<size_t>(s) * p.max_pages + pages_of(p.ctx[s], p.P) + (e - need0[s])] =
           p.ring[in_ring(static_cast<unsigned>(head) + e, p.F)];
     }
   }
   // tokens: a page that was there before comes from the table, a new one from the ring
-  for (int t = gtid; t < p.T; t += gsize) {
+  for (unsigned t = gtid; t < static_cast<unsigned>(p.T); t += gsize) {
     int pos = -1, slot = -1;
-    if (t < total) {
-      const int lo = owner(tok0, t);
+    if (t < static_cast<unsigned>(total)) {
+      const int lo = owner(tok0, static_cast<int>(t));
       const int c = p.ctx[lo];
-      pos = c + t - tok0[lo];
+      pos = c + (static_cast<int>(t) - tok0[lo]);
       const int old = pages_of(c, p.P), j = pos / p.P;
       const int page = j < old ? p.bt[static_cast<size_t>(lo) * p.max_pages + j]
                                : p.ring[in_ring(static_cast<unsigned>(head) + need0[lo] + (j - old), p.F)];
