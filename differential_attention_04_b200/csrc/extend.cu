@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kJoinThreads) extend_join_kernel(const ExtendA
         y.w = fmaf(y.w, i1, z.w * i2);
         ss += y.x * y.x + y.y * y.y + y.z * y.z + y.w * y.w;
       }
-      const float gsc = (1.f - a.lambda_init) * rsqrtf(sum_of(ss) / DV + a.eps);
+      const float gsc = norm_factor(sum_of(ss) / DV, a.eps, a.lambda_init);
       __nv_bfloat16* o = out_row(r);
 #pragma unroll
       for (int i = 0; i < NV / 2; ++i) {
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kJoinThreads) extend_join_kernel(const ExtendA
 #pragma unroll
     for (int g = 0; g < kJoinWarps; ++g) ss += red[0][g];
     if (tid < DV) {
-      const float gsc = (1.f - a.lambda_init) * rsqrtf(ss / DV + a.eps);
+      const float gsc = norm_factor(ss / DV, a.eps, a.lambda_init);
       out_row(r)[tid] = __float2bfloat16_rn(y * gsc * a.rms_w[tid]);
     }
     __syncthreads();  // the next row reuses the shared memory

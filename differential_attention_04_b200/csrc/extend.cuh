@@ -125,6 +125,13 @@ __host__ __device__ inline PlanLayout plan_layout(const ExtendShape& n) {
   return l;
 }
 
+// What a row is multiplied with behind its norm.  A row of zeros (one that sees no
+// key) stays one with eps = 0 too, where 1 / sqrt(0) would make it NaN.
+__device__ __forceinline__ float norm_factor(float mean_square, float eps, float lambda_init) {
+  const float x = mean_square + eps;
+  return x > 0.f ? (1.f - lambda_init) * rsqrtf(x) : x;  // (x: 0, or a NaN that stays one)
+}
+
 // A record: (m1, l1, m2, l2) of every row, then per row both maps' sums over 2d channels.
 __host__ __device__ inline size_t record_floats(int rows, int d) {
   return static_cast<size_t>(rows) * (4 + 4 * d);

@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 2) extend_narrow_kernel(const Extend
           float ss = 0.f;
 #pragma unroll
           for (int w = 0; w < 2 * kPairs; ++w) ss += s_ss[w][r];
-          const float gsc = (1.f - a.lambda_init) * rsqrtf(ss / DV + a.eps);
+          const float gsc = norm_factor(ss / DV, a.eps, a.lambda_init);
           const size_t row = static_cast<size_t>(cur.rq.q0 + r / G) * H + cur.hk * G + r % G;
 #pragma unroll
           for (int e = 0; e < E; ++e) {

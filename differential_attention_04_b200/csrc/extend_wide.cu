@@ -543,8 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_bar_sync(1, 128);  // every warp's outgoing copy is done with the rows the output tile reuses
       // a partner that is gone sends nothing: this CTA leaves at the next vote, before its barriers are armed again
       if (!mbar_wait_acq_cluster(&bars->ss_full, ke & 1, wdrain) || !got_half) bars->abort = 1;
-      const float rs = rsqrtf((ss + ssx[r]) / static_cast<float>(C::DV) + p.eps);
-      const float gsc = (1.0f - p.lambda_init) * rs;
+      const float gsc = norm_factor((ss + ssx[r]) / static_cast<float>(C::DV), p.eps, p.lambda_init);
       // bf16 tile [64-column block][128 rows][64 columns], 128-byte swizzle, in the staging stage
       const uint32_t sout = smem_u32(stage);
 #pragma unroll

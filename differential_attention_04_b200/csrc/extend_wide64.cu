@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ssx[map * kBM + r] = ss;
       named_bar_sync(1 + quarter, 64);  // and both sums of squares; both buffers have been read
       ss += ssx[(map ^ 1) * kBM + r];
-      const float gsc = (1.0f - p.lambda_init) * rsqrtf(ss / static_cast<float>(C::DV) + p.eps);
+      const float gsc = norm_factor(ss / static_cast<float>(C::DV), p.eps, p.lambda_init);
       // The warp's 32 rows of 64 channels as bf16 through its part of the buffer, to be written row by row.
       const uint32_t out = smem_u32(swap + (map * kBM + quarter * 32) * D);
 #pragma unroll

@@ -40,3 +40,37 @@ def test_step_with_as_many_rows_as_an_index_can_count(T):
     for got, w in ((pos, want[5]), (slots, want[6])):
         assert got.numel() == T and got[:24].tolist() == list(w)
         assert all(bool((x == -1).all()) for x in got[24:].split(1 << 28))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,kv,H,G", [
+    ([4, 1, 1], [0, 0, 30], 2, 1),          # few rows
+    ([7, 2], [2, 150], 4, 2),               # up to 14 rows: both forms of the few-row kernel
+    ([300, 20], [170, 20], 2, 1),           # many rows, some of them blind
+    ([260], [0], 2, 1),                     # and all of them
+    ([3000], [1500], 1, 1), ([40], [6000], 1, 1), ([6], [20000], 1, 1)])  # rows whose keys are split among workers
+@pytest.mark.parametrize("causal", [True, False])
+def test_extend_without_an_epsilon(d, new, kv, H, G, causal):
+    """eps = 0: rows that see no key are zeros, the others are normalised to their mean square alone."""
+    page, T, Hkv = 16, sum(new), H // G
+    held = [-(-x // page) for x in kv]
+    table, at = np.full((len(kv), max(max(held), 1)), -1), 0
+    for s, n in enumerate(held):
+        table[s, :n] = np.arange(at, at + n)[::-1]
+        at += n
+    g = torch.Generator(device=DEV).manual_seed(T)
+    bf = lambda *s: torch.randn(*s, generator=g, device=DEV).bfloat16()
+    q, kc, vc = bf(T, H, 2, d), bf(at + 1, page, Hkv, 2, d), bf(at + 1, page, Hkv, 2 * d)
+    lam, w = torch.tensor([0.3], device=DEV), torch.linspace(0.5, 1.5, 2 * d, device=DEV)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    plan = api.extend_plan(i32(cu), i32(kv), T, H, Hkv, d, max(new), causal)
+    out = api.diffattn_extend(q, kc, vc, i32(table), plan, lam, 0.4, w, 0.0)
+    assert bool(torch.isfinite(out.float()).all())
+    # (mean of (y / w)^2: (1 - 0.4)^2 where there are keys; the rounding to bf16 is at most 2^-8 of each y)
+    ms = (out.double() / w.double()).square().mean(-1)
+    for s, (n, L) in enumerate(zip(new, kv)):
+        rows = ms[cu[s]:cu[s + 1]]
+        blind = n if L == 0 else max(0, n - L) if causal else 0
+        assert bool((out[cu[s]:cu[s] + blind] == 0).all())
+        # float32 sums of 2d squares and their rsqrt: below 2^-12
+        assert bool(((rows[blind:] / 0.36 - 1).abs() <= 2 * 2.0 ** -8 + 2.0 ** -16 + 2.0 ** -12).all())
