@@ -487,6 +487,14 @@ def _i32(name: str, t: torch.Tensor, *shape: int) -> None:
         raise ValueError(f"{name} must be int32 of shape {shape}")
 
 
+def _int32(name: str, x) -> int:
+    """x as the library takes its sizes and switches (ctypes would drop the bits above)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits")
+    return x
+
+
 def _same(name: str, t: torch.Tensor, shape, dtype) -> None:
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}")
@@ -511,12 +519,13 @@ def paged_step(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torc
     _need(ctx_lens.dim() == 1 and block_table.dim() == 2 and free_pages.dim() == 1,
           "ctx_lens must be [S], block_table [S, max_pages] and free_pages [ring_size]")
     S, max_pages = block_table.shape
-    T = int(num_tokens)
+    T, page_size = _int32("num_tokens", num_tokens), _int32("page_size", page_size)
     _need(T >= 0, "num_tokens must not be negative")
     _i32("ctx_lens", ctx_lens, S)
     _i32("new_lens", new_lens, S)
     _i32("block_table", block_table, S, max_pages)
-    F = free_pages.numel()
+    F = _int32("ring_size", free_pages.numel())
+    _int32("max_pages", max_pages)
     _i32("free_pages", free_pages, F)
     _i32("pool", pool, 2)
     if pool_out is None:
@@ -534,7 +543,7 @@ def paged_step(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torc
     cu_q, kv_lens, positions, slots, info = out
     _launch("diffattn_paged_step", ts,
             ctx_lens.data_ptr(), new_lens.data_ptr(), S, block_table.data_ptr(), max_pages, free_pages.data_ptr(), F,
-            pool.data_ptr(), pool_out.data_ptr(), int(page_size), T, cu_q.data_ptr(), kv_lens.data_ptr(),
+            pool.data_ptr(), pool_out.data_ptr(), page_size, T, cu_q.data_ptr(), kv_lens.data_ptr(),
             positions.data_ptr(), slots.data_ptr(), info.data_ptr())
     return cu_q, kv_lens, positions, slots, info
 
@@ -544,9 +553,11 @@ def rope_table_scaled(N: int, rot: int, base: float = 10000.0, scaling: int = RO
                       device=None) -> torch.Tensor:
     """(cos, sin) of n * theta'_j for n < N, j < rot/2 with the frequencies scaled for long contexts
     (ROPE_LINEAR, ROPE_NTK, ROPE_YARN; the last also scales cos and sin): float32 [N, rot/2, 2]."""
+    N, rot, scaling = _int32("N", N), _int32("rot", rot), _int32("scaling", scaling)
+    orig_len = _int32("orig_len", orig_len)
     t = torch.empty((N, rot // 2, 2), dtype=torch.float32, device=device or torch.device("cuda"))
-    _launch("diffattn_rope_table_scaled", (t,), int(N), int(rot), float(base), int(scaling), float(factor),
-            int(orig_len), float(beta_fast), float(beta_slow), _ptr(t))
+    _launch("diffattn_rope_table_scaled", (t,), N, rot, float(base), scaling, float(factor), orig_len,
+            float(beta_fast), float(beta_slow), _ptr(t))
     return t
 
 
@@ -556,7 +567,7 @@ def _rope_args(d, positions, table, T):
         raise ValueError("table must be float32 [n_pos, rot/2, 2] with rot <= d")
     if positions.dtype is not torch.int32 or positions.numel() != T:
         raise ValueError("positions must be int32 with one entry per row")
-    return ts[0], 2 * ts[1]
+    return _int32("n_pos", ts[0]), 2 * ts[1]
 
 
 def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table: torch.Tensor,
@@ -574,7 +585,7 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table
         return tuple(out)
     qs = q.shape
     _need(len(qs) >= 4 and qs[-2] == 2, "q must be [..., H, 2, d]")
-    H, d = qs[-3], qs[-1]
+    H, d, layout = qs[-3], qs[-1], _int32("layout", layout)
     T = positions.numel()
     _need(q.numel() == T * H * 2 * d, "positions must be int32 with one entry per row")
     dt = BF16 if q.dtype == torch.bfloat16 else F32 if q.dtype == torch.float32 else None
@@ -594,7 +605,7 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table
         _same("k'", ko, ks, k.dtype)
         ts += (k, ko)
     _launch("diffattn_rope", ts, q.data_ptr(), _ptr(k), positions.data_ptr(), table.data_ptr(), n_pos, T, H, H_kv, d,
-            rot, dt, int(layout), int(bool(inverse)), qo.data_ptr(), _ptr(ko))
+            rot, dt, layout, int(bool(inverse)), qo.data_ptr(), _ptr(ko))
     return qo, ko
 
 
@@ -605,7 +616,7 @@ def _cache_shapes(k_cache, v_cache, d, dtype):
         raise ValueError("k_cache must be [num_pages, page_size, H_kv, 2, d] of q's dtype")
     P, ps, H_kv, _, _ = s
     _same("v_cache", v_cache, (P, ps, H_kv, 2 * d), dtype)
-    return P, ps, H_kv
+    return _int32("num_pages", P), _int32("page_size", ps), H_kv
 
 
 def _rows(q):
@@ -629,6 +640,7 @@ def kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torc
                       fast.kv_append(q, k, v, positions, slots, table, k_cache, v_cache, layout, out)):
         return out
     T, H, d = _rows(q)
+    layout = _int32("layout", layout)
     num_pages, page_size, H_kv = _cache_shapes(k_cache, v_cache, d, torch.bfloat16)
     _same("k", k, (T, H_kv, 2, d), torch.bfloat16)
     _same("v", v, (T, H_kv, 2 * d), torch.bfloat16)
@@ -642,7 +654,7 @@ def kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torc
         ts += (positions, table)
     _launch("diffattn_kv_append", ts, q.data_ptr(), k.data_ptr(), v.data_ptr(),
             None if table is None else positions.data_ptr(), slots.data_ptr(), _ptr(table), n_pos, T, H, H_kv, d, rot,
-            int(layout), num_pages, page_size, out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr())
+            layout, num_pages, page_size, out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr())
     return out
 
 
@@ -664,7 +676,8 @@ def extend_plan(cu_q: torch.Tensor, kv_lens: torch.Tensor, num_tokens: int, H: i
     S = kv_lens.numel()
     _i32("cu_q", cu_q, S + 1)
     _i32("kv_lens", kv_lens, S)
-    n = (S, int(num_tokens), int(H), int(H_kv), int(d), int(max_new))
+    n = tuple(_int32(name, x) for name, x in (("S", S), ("num_tokens", num_tokens), ("H", H), ("H_kv", H_kv), ("d", d),
+                                              ("max_new", max_new)))
     need = int(lib().diffattn_extend_plan_size(*n))
     if buf is None:
         buf = torch.empty(max(need, 16), dtype=torch.uint8, device=kv_lens.device)
@@ -674,7 +687,7 @@ def extend_plan(cu_q: torch.Tensor, kv_lens: torch.Tensor, num_tokens: int, H: i
 
 
 def extend_workspace_size(plan: ExtendPlan) -> int:
-    return int(lib().diffattn_extend_workspace_size(*plan[1:]))
+    return int(lib().diffattn_extend_workspace_size(*(_int32(n, x) for n, x in zip(plan._fields[1:], plan[1:]))))
 
 
 def diffattn_extend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -694,6 +707,8 @@ def diffattn_extend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     bs = block_table.shape
     if block_table.dtype is not torch.int32 or len(bs) != 2 or bs[0] != plan.S:
         raise ValueError("block_table must be int32 [S, max_pages] with the plan's S")
+    S, max_new, max_pages = _int32("S", plan.S), _int32("max_new", plan.max_new), _int32("max_pages", bs[1])
+    mode = _int32("mode", mode)
     _scalar_f32("lam", lam)
     _f32("rms_w", rms_w, 2 * d)
     if out is None:
@@ -702,9 +717,9 @@ def diffattn_extend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     if workspace is None:
         workspace = torch.empty(max(extend_workspace_size(plan), 16), dtype=torch.uint8, device=q.device)
     _launch("diffattn_extend", (q, k_cache, v_cache, block_table, plan.buf, lam, rms_w, workspace, out),
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), bs[1], num_pages, page_size,
-            plan.buf.data_ptr(), plan.buf.nbytes, plan.S, T, H, H_kv, d, plan.max_new, lam.data_ptr(),
-            float(lambda_init), rms_w.data_ptr(), float(eps), int(mode), out.data_ptr(), workspace.data_ptr(),
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), max_pages, num_pages,
+            page_size, plan.buf.data_ptr(), plan.buf.nbytes, S, T, H, H_kv, d, max_new, lam.data_ptr(),
+            float(lambda_init), rms_w.data_ptr(), float(eps), mode, out.data_ptr(), workspace.data_ptr(),
             workspace.nbytes)
     return out
 
