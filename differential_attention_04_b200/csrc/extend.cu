@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
     if (is_wide) v.tiles = (nq + tpt - 1) / tpt;
     const PlanSums at = plan_scan(v, sm, total);
     if (v.reqs) {
-      const int i = carry.reqs + at.reqs;
+      const int i = DA_CHECK(status, carry.reqs + at.reqs < n.S) ? carry.reqs + at.reqs : 0;
       narrow[i] = NarrowReq{q0, nq, L, s};
       npre[i] = carry.units + at.units;
     }
@@ -182,7 +182,9 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
   for (int x = tid; x < ntiles; x += kPlanThreads) {
     const WideTile t = wide[x];
     for (int hk = 0; hk < n.H_kv; ++hk)
-      items[item_index(t, x, hk)] = WideItem{t.tok0, t.ntok, t.lim0, t.units, t.L, t.s, hk, x};
+      if (DA_CHECK(status, item_index(t, x, hk) >= 0 &&
+                               item_index(t, x, hk) < static_cast<long long>(lay.max_tiles) * n.H_kv))
+        items[item_index(t, x, hk)] = WideItem{t.tok0, t.ntok, t.lim0, t.units, t.L, t.s, hk, x};
   }
   const long long nitems = static_cast<long long>(ntiles) * n.H_kv;
   if (tid == 0) s_rounds = W[1] > 0 ? static_cast<int>(nitems / W[1]) : 0;
@@ -327,8 +329,13 @@ __global__ void __launch_bounds__(kJoinThreads) extend_join_kernel(const ExtendA
   const WorkTail tl = pv.tails[w];
   if (tl.parts == 0) return;
   const int G = a.n.H / a.n.H_kv;
-  const int tok0 = is_wide ? pv.wide[tl.at].tok0 : pv.narrow[tl.at].q0;
-  const int R = (is_wide ? pv.wide[tl.at].ntok : pv.narrow[tl.at].n) * G;
+  // debug builds: the parts' records are the class's workers', and the rows a request's
+  if (!DA_CHECK(status, tl.parts > 1 && tl.member >= 0 && tl.member < tl.parts - 1 && w >= tl.member &&
+                            w - tl.member + tl.parts <= (is_wide ? wide_workers(a.n.d) : kNarrowWorkers) &&
+                            tl.hk >= 0 && tl.hk < a.n.H_kv))
+    return;
+  const int tok0 = is_wide ? wide_at(pv.wide, tl.at, a.n, status).tok0 : narrow_at(pv.narrow, tl.at, a.n, status).q0;
+  const int R = (is_wide ? wide_at(pv.wide, tl.at, a.n, status).ntok : narrow_at(pv.narrow, tl.at, a.n, status).n) * G;
   const int rows = is_wide ? kWideRows : narrow_rows(a.n);
   const float* recs = is_wide ? wrecs : nrecs;
   const size_t rec = record_floats(rows, D);

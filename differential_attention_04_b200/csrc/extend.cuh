@@ -24,6 +24,7 @@
 //     joining kernel adds up in order.
 #pragma once
 
+#include "common.cuh"
 #include "internal.h"
 
 namespace diffattn {
@@ -172,7 +173,35 @@ __device__ inline bool plan_fits(const void* plan, const ExtendShape& n, const U
                   p.d == n.d && p.max_new == n.max_new &&
                   h->units[0] <= most.units[0] && h->units[1] <= most.units[1];
   if (!ok) atomicCAS(status, 0, 6);
-  return ok;
+  // debug builds: what its lists and ranges are indexed with
+  return ok && DA_CHECK(status, h->tiles >= 0 && h->tiles <= plan_layout(n).max_tiles && h->workers[0] >= 0 &&
+                                    h->workers[0] <= kNarrowWorkers && h->workers[1] >= 0 &&
+                                    h->workers[1] <= wide_workers(n.d) && h->rounds >= 0 &&
+                                    static_cast<long long>(h->rounds) * h->workers[1] <=
+                                        static_cast<long long>(h->tiles) * n.H_kv);
+}
+// Entries of a plan's lists.  Debug builds check the index and everything that is
+// computed from the entry (rows of q and o, of the block table, a key head); one
+// that is out of range counts as an entry without rows and keys.
+__device__ __forceinline__ NarrowReq narrow_at(const NarrowReq* list, int at, const ExtendShape& n, int* status) {
+  if (!DA_CHECK(status, at >= 0 && at < n.S)) return NarrowReq{0, 0, 0, 0};
+  const NarrowReq r = list[at];
+  return DA_CHECK(status, r.q0 >= 0 && r.n >= 0 && r.n <= n.T - r.q0 &&
+                              static_cast<long long>(r.n) * (n.H / n.H_kv) <= narrow_rows(n) && r.L >= 0 &&
+                              r.L <= kMaxKeys && r.s >= 0 && r.s < n.S)
+             ? r
+             : NarrowReq{0, 0, 0, 0};
+}
+__device__ __forceinline__ WideItem wide_at(const WideItem* list, int at, const ExtendShape& n, int* status) {
+  if (!DA_CHECK(status, at >= 0 && at < static_cast<long long>(plan_layout(n).max_tiles) * n.H_kv))
+    return WideItem{0, 0, -1, 1, 0, 0, 0, 0};
+  const WideItem t = list[at];
+  return DA_CHECK(status, t.tok0 >= 0 && t.ntok >= 0 && t.ntok <= n.T - t.tok0 &&
+                              static_cast<long long>(t.ntok) * (n.H / n.H_kv) <= kWideRows && t.units >= 1 &&
+                              t.units <= kMaxKeys / kUnit + 1 && t.L >= 0 && t.L <= kMaxKeys && t.s >= 0 &&
+                              t.s < n.S && t.hk >= 0 && t.hk < n.H_kv)
+             ? t
+             : WideItem{0, 0, -1, 1, 0, 0, 0, 0};
 }
 __device__ inline PlanView plan_view(const void* plan, const ExtendShape& n, int cls) {
   const PlanLayout l = plan_layout(n);

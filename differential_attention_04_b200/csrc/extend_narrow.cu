@@ -112,11 +112,11 @@ struct Cursor {
   __device__ void count_units() { units = rq.L <= 0 ? 1 : (rq.L - 1) / kUnit + 1; }
   __device__ explicit Cursor(const WorkStart& st) : rq(st.rq), at(st.at), hk(st.hk), unit(st.unit) { count_units(); }
   // The item behind this one (only called while the worker has units left).
-  __device__ void next(const NarrowReq* list, int H_kv) {
+  __device__ void next(const NarrowReq* list, const ExtendShape& n, int* status) {
     unit = 0;
-    if (++hk == H_kv) {
+    if (++hk == n.H_kv) {
       hk = 0;
-      rq = list[++at];
+      rq = narrow_at(list, ++at, n, status);
       count_units();
     }
   }
@@ -139,6 +139,16 @@ __global__ void __launch_bounds__(kThreads, 2) extend_narrow_kernel(const Extend
   const WorkStart st = pv.starts[blockIdx.x];  // read beside the header: the first loads are one chain of trips to L2
   if (!plan_fits(a.plan, a.n, most, status)) return;
   if (st.count == 0) return;
+#ifdef DIFFATTN_DEBUG
+  {  // the range begins in the request that its entry names
+    const NarrowReq r = narrow_at(pv.narrow, st.at, a.n, status);
+    const Cursor c(st);
+    if (!da_check(status, st.count > 0 && st.count <= pv.head->units[0] && r.q0 == st.rq.q0 && r.n == st.rq.n &&
+                              r.L == st.rq.L && r.s == st.rq.s && st.hk >= 0 && st.hk < a.n.H_kv && st.unit >= 0 &&
+                              st.unit < c.units))
+      return;
+  }
+#endif
   const int causal = pv.head->causal;
   const int H = a.n.H, H_kv = a.n.H_kv, G = H / H_kv;
   const uint32_t ring = smem_u32(smem) + pair * C::STAGES * C::STAGE;
@@ -155,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 2) extend_narrow_kernel(const Extend
   int issued = 0;
   auto issue = [&]() {
     if (issued < steps) {
-      if (issued > 0 && issued % SPU == 0 && ++ld.unit == ld.units) ld.next(pv.narrow, H_kv);
+      if (issued > 0 && issued % SPU == 0 && ++ld.unit == ld.units) ld.next(pv.narrow, a.n, status);
       const int L = min(ld.rq.L, max_keys);
 #pragma unroll
       for (int x = 0; x < SL; ++x) {
@@ -218,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 2) extend_narrow_kernel(const Extend
     // the item behind this one: its request is read now and its queries before the merge, so that neither is waited for
     Cursor nx = cur;
     const bool more = left > take;
-    if (more) nx.next(pv.narrow, H_kv);
+    if (more) nx.next(pv.narrow, a.n, status);
     // this thread's columns of S^T and O^T and the last keys that their rows see
     int lim[NT][2];
     float o[NT][CT][4], mx[NT][2], l[NT][2];

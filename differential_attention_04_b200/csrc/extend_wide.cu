@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!plan_fits(p.plan, p.n, p.most, p.status)) return;  // the same for both CTAs of the cluster
   const PlanView pv = plan_view(p.plan, p.n, 1);
   Walk wk;
-  if (!wk.begin(pv, blockIdx.x >> 1)) return;  // and this too
+  if (!wk.begin(pv, blockIdx.x >> 1, p)) return;  // and this too
   const int causal = pv.head->causal;
   const int H = p.n.H, G = H / p.n.H_kv, tpt = kBM / G;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         blk * 64, 2 * wk.t.hk + static_cast<int>(rank), row, 0);
         }
       }
-      if (!ok || !wk.next(pv)) break;
+      if (!ok || !wk.next(pv, p)) break;
     }
     // nothing may still be landing in shared memory when the CTA exits (after an
     // abort no product may have waited for the last Q either)
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&bars->v_full[st]);
         }
       }
-      if (!ok || !wk.next(pv)) break;
+      if (!ok || !wk.next(pv, p)) break;
     }
     for (int j = max(0, gv - 2); j < gv; ++j) mbar_wait(&bars->v_full[j & 1], (j >> 1) & 1, wdrain);
     __syncwarp();
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j > 0) ok = issue_pv(j == 1);
         }
         if (ok) ok = issue_pv(wk.take == 1);
-        if (!ok || !wk.next(pv)) break;
+        if (!ok || !wk.next(pv, p)) break;
       }
       // drain: every issued MMA has completed before tensor memory is read or freed
       umma_commit(&bars->mma_done);
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->epi_free);
-    } while (wk.next(pv));
+    } while (wk.next(pv, p));
   }
 
   if (warp >= 4) {
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // complete the barrier without it and leave it waiting for good.)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->tile_full);
-    } while (wk.next(pv));
+    } while (wk.next(pv, p));
   }
 
   tc_fence_before();

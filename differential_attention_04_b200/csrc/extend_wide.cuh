@@ -54,42 +54,45 @@ struct Walk {
   WideItem t;
   int at, unit, take, left;  // left: units of the range from this segment on
   int worker, workers, whole_end;
-  __device__ bool begin(const PlanView& pv, int w) {  // false: there is no work
+  __device__ WideItem item(const PlanView& pv, const WideParams& p) const { return wide_at(pv.wide, at, p.n, p.status); }
+  __device__ bool begin(const PlanView& pv, int w, const WideParams& p) {  // false: there is no work
     worker = w;
     workers = pv.head->workers[1];
     whole_end = pv.head->rounds * workers;
     left = pv.starts[w].count;
-    if (w >= workers || whole_end == 0) return open_range(pv);
+    if (!DA_CHECK(p.status, left <= pv.head->units[1] * p.n.H_kv)) left = 0;
+    if (w >= workers || whole_end == 0) return open_range(pv, p);
     at = w;
-    open_whole(pv);
+    open_whole(pv, p);
     return true;
   }
-  __device__ void open_whole(const PlanView& pv) {
-    t = pv.wide[at];
+  __device__ void open_whole(const PlanView& pv, const WideParams& p) {
+    t = item(pv, p);
     unit = 0;
     take = t.units;
   }
-  __device__ bool open_range(const PlanView& pv) {
+  __device__ bool open_range(const PlanView& pv, const WideParams& p) {
     whole_end = 0;
     if (left <= 0) return false;
     const WorkStart st = pv.starts[worker];
     at = st.at;
     unit = st.unit;
-    t = pv.wide[at];
+    t = item(pv, p);
+    if (!DA_CHECK(p.status, unit >= 0 && unit < t.units)) return false;
     take = min(left, t.units - unit);
     return true;
   }
-  __device__ bool next(const PlanView& pv) {  // false: that was the last segment
+  __device__ bool next(const PlanView& pv, const WideParams& p) {  // false: that was the last segment
     if (whole_end) {
       at += workers;
-      if (at >= whole_end) return open_range(pv);
-      open_whole(pv);
+      if (at >= whole_end) return open_range(pv, p);
+      open_whole(pv, p);
       return true;
     }
     left -= take;
     if (left <= 0) return false;
     ++at;
-    t = pv.wide[at];
+    t = item(pv, p);
     unit = 0;
     take = min(left, t.units);
     return true;
@@ -107,6 +110,7 @@ struct TileBoxes {
   __device__ int row(const WideParams& p, const WideItem& t, int key0, int boxes, int lane) const {
     if (lane >= boxes) return 0;
     const int key = key0 + (lane << shift);
+    if (!DA_CHECK(p.status, (key >> p.page_shift) < p.max_pages)) return -kUnit;
     const int page = p.block_table[static_cast<size_t>(t.s) * p.max_pages + (key >> p.page_shift)];
     if (page < 0 || page >= p.num_pages) {
       atomicCAS(p.status, 0, 6);

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!plan_fits(p.plan, p.n, p.most, p.status)) return;
   const PlanView pv = plan_view(p.plan, p.n, 1);
   Walk wk;
-  if (!wk.begin(pv, blockIdx.x)) return;
+  if (!wk.begin(pv, blockIdx.x, p)) return;
   const int causal = pv.head->causal;
   const int H = p.n.H, G = H / p.n.H_kv, tpt = kBM / G;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           2 * wk.t.hk + m, row, 0);
           }
         }
-        if (!ok || !wk.next(pv)) break;
+        if (!ok || !wk.next(pv, p)) break;
       }
       // nothing may still be landing in shared memory when the CTA exits (after an
       // abort no product may have waited for the last Q either)
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&bars->v_full[st]);
           }
         }
-        if (!ok || !wk.next(pv)) break;
+        if (!ok || !wk.next(pv, p)) break;
       }
       for (int j = max(0, gv - 2); j < gv; ++j) mbar_wait(&bars->v_full[j & 1], (j >> 1) & 1, wdrain);
       __syncwarp();
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_commit(&bars->pv_done[m][b]);
             if (b == 1) umma_commit(&bars->v_empty[st]);
           }
-          if (!ok || !wk.next(pv)) break;
+          if (!ok || !wk.next(pv, p)) break;
         }
         // drain: every issued MMA has completed before tensor memory is read or freed
         umma_commit(&bars->mma_done);
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();  // the buffer is read before the next segment's sums replace it
-    } while (wk.next(pv));
+    } while (wk.next(pv, p));
   }
 
   tc_fence_before();

@@ -39,6 +39,7 @@ struct StepParams {
   int P, T;
   int *cu_q, *kv, *pos, *slots, *info;
   int write_pool;
+  int* status;  // debug builds
 };
 
 struct Sums {
@@ -185,13 +186,15 @@ __global__ void __launch_bounds__(kStepThreads) paged_step_kernel(const StepPara
     const unsigned taken = static_cast<unsigned>(carry.need), back = static_cast<unsigned>(carry.rel);
     for (unsigned e = gtid; e < back; e += gsize) {
       const int s = owner(rel0, static_cast<int>(e));
-      p.ring[in_ring(static_cast<unsigned>(head) + count + e, p.F)] =
-          p.bt[static_cast<size_t>(s) * p.max_pages + (e - rel0[s])];
+      const unsigned to = in_ring(static_cast<unsigned>(head) + count + e, p.F), col = e - rel0[s];
+      if (DA_CHECK(p.status, to < static_cast<unsigned>(p.F) && col < static_cast<unsigned>(p.max_pages)))
+        p.ring[to] = p.bt[static_cast<size_t>(s) * p.max_pages + col];
     }
     for (unsigned e = gtid; e < taken; e += gsize) {
       const int s = owner(need0, static_cast<int>(e));
-      p.bt[static_cast<size_t>(s) * p.max_pages + pages_of(p.ctx[s], p.P) + (e - need0[s])] =
-          p.ring[in_ring(static_cast<unsigned>(head) + e, p.F)];
+      const unsigned from = in_ring(static_cast<unsigned>(head) + e, p.F), col = pages_of(p.ctx[s], p.P) + (e - need0[s]);
+      if (DA_CHECK(p.status, from < static_cast<unsigned>(p.F) && col < static_cast<unsigned>(p.max_pages)))
+        p.bt[static_cast<size_t>(s) * p.max_pages + col] = p.ring[from];
     }
   }
   // tokens: a page that was there before comes from the table, a new one from the ring
@@ -202,8 +205,9 @@ __global__ void __launch_bounds__(kStepThreads) paged_step_kernel(const StepPara
       const int c = p.ctx[lo];
       pos = c + (static_cast<int>(t) - tok0[lo]);
       const int old = pages_of(c, p.P), j = pos / p.P;
-      const int page = j < old ? p.bt[static_cast<size_t>(lo) * p.max_pages + j]
-                               : p.ring[in_ring(static_cast<unsigned>(head) + need0[lo] + (j - old), p.F)];
+      const unsigned from = in_ring(static_cast<unsigned>(head) + need0[lo] + max(j - old, 0), p.F);
+      const bool fits = DA_CHECK(p.status, pos >= c && (j < old ? j < p.max_pages : from < static_cast<unsigned>(p.F)));
+      const int page = !fits ? -1 : j < old ? p.bt[static_cast<size_t>(lo) * p.max_pages + j] : p.ring[from];
       // a page number that is no page's stays out of every cache's range
       slot = page < 0 ? -1 : static_cast<int>(min(static_cast<long long>(page) * p.P + pos % p.P, 0x7fffffffll));
     }
@@ -226,7 +230,8 @@ cudaError_t launch_paged_step(const int* ctx_lens, const int* new_lens, int S, i
                               int* free_pages, int ring_size, const int* pool, int* pool_out, int page_size, int T,
                               int* cu_q, int* kv_lens, int* positions, int* slots, int* info, cudaStream_t stream) {
   StepParams p = {ctx_lens, new_lens, S,    block_table, max_pages, free_pages, ring_size, pool,
-                  pool_out, page_size, T,   cu_q,        kv_lens,   positions,  slots,     info,       0};
+                  pool_out, page_size, T,   cu_q,        kv_lens,   positions,  slots,     info,       0,
+                  debug_status()};
   const size_t smem = static_cast<size_t>(3 * S + 1) * sizeof(int);
   cudaError_t e = cudaSuccess;
   if (smem > 48 * 1024) {

@@ -115,6 +115,10 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_rows_kernel(const RopePa
   const int second = rotated ? half : VEC;  // of a unit's two loads, behind the first
   const bool has_b = HALF && c0 + second < p.d;
   constexpr int NP = HALF ? VEC : VEC / 2;  // pairs of a unit
+  // debug builds: the unit lies in its row, and its pairs in the table's
+  if (!DA_CHECK(p.status, c0 + VEC <= p.d && (!has_b || c0 + second + VEC <= p.d) &&
+                              (!rotated || (HALF ? c0 : c0 / 2) + NP <= half)))
+    return;
   const int pos = p.table ? p.positions[t] : 0;
   // rows of this token's keys and values: its own, or its slot of the cache
   const int slot = p.slots ? p.slots[t] : t;
