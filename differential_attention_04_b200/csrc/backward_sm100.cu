@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 // One warp per (batch, token, head) row: O = O_1 + c O_2 from the
 // statistics pass, the RMSNorm backward G, D_1 = G . O_1 and D_2 = c G . O_2
 // (with G rounded to bf16, as the tensor cores see it), and per-CTA sums of
-// dw and dlambda added to the outputs at the end.
+// dw and dlambda, which bwd_sums_kernel adds up in a fixed order.
 template <int D>
 __global__ void __launch_bounds__(256) bwd_prep_kernel(const float* __restrict__ o_maps,
                                                        const __nv_bfloat16* __restrict__ dy,
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const float* __restrict__
                                                        const float* __restrict__ lambda_ptr, int mode, float dcoef,
                                                        float lambda_init, float eps, int B, int N, int H, int n_pad,
                                                        __nv_bfloat16* __restrict__ G, float4* __restrict__ stats,
-                                                       float* __restrict__ dlambda, float* __restrict__ drms_w,
+                                                       float* __restrict__ part_dl, float* __restrict__ part_dw,
                                                        int* dbg) {
   constexpr int DV = 2 * D;
   constexpr int E = DV / 32;  // columns per lane, contiguous
@@ -521,14 +521,50 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const float* __restrict__
     float a = 0.f;
 #pragma unroll
     for (int w8 = 0; w8 < 8; ++w8) a += s_dw[w8][c];
-    atomicAdd(drms_w + c, a);
+    part_dw[static_cast<size_t>(blockIdx.x) * DV + c] = a;
   }
   if (threadIdx.x == 0) {
     float a = 0.f;
 #pragma unroll
     for (int w8 = 0; w8 < 8; ++w8) a += s_dl[w8];
-    atomicAdd(dlambda, dcoef * a);
+    part_dl[blockIdx.x] = dcoef * a;
   }
+}
+
+// drms_w and dlambda from the prep kernel's n CTAs: a block for every 32
+// columns, a warp for every 32nd CTA, the warps' sums added in their order (the
+// last block does the same for dlambda, a thread a CTA).  So both repeat bit for
+// bit; atomics in the CTAs' order of arrival left 10^-4 of a small sum open.
+// 2.4 MB from L2 at most.
+template <int D>
+__global__ void __launch_bounds__(1024) bwd_sums_kernel(const float* __restrict__ part_dl,
+                                                        const float* __restrict__ part_dw, int n,
+                                                        float* __restrict__ dlambda, float* __restrict__ drms_w) {
+  constexpr int DV = 2 * D;
+  __shared__ float sm[32][33];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool cols = blockIdx.x < DV / 32;
+  const int c = 32 * blockIdx.x + lane;
+  float a = 0.f;
+  if (cols) {
+#pragma unroll 4
+    for (int i = warp; i < n; i += 32) a += part_dw[static_cast<size_t>(i) * DV + c];
+  } else {
+    for (int i = threadIdx.x; i < n; i += 1024) a += part_dl[i];
+  }
+  sm[warp][lane] = a;
+  __syncthreads();
+  if (warp > 0) return;
+  float t = 0.f;
+#pragma unroll
+  for (int w = 0; w < 32; ++w) t += sm[w][lane];
+  if (cols) {
+    drms_w[c] = t;
+    return;
+  }
+#pragma unroll
+  for (int s = 16; s >= 1; s >>= 1) t += __shfl_xor_sync(0xffffffffu, t, s);
+  if (lane == 0) *dlambda = t;
 }
 
 template <int D, int KIND>
@@ -553,9 +589,7 @@ cudaError_t launch_bwd_sm100_d(const BwdTcMaps& m, const void* dy, int B, int N,
   float* o_maps = reinterpret_cast<float*>(ws + L.off_omaps);
   __nv_bfloat16* G = reinterpret_cast<__nv_bfloat16*>(ws + L.off_g);
   float4* stats = reinterpret_cast<float4*>(ws + L.off_stats);
-  cudaError_t e = cudaMemsetAsync(drms_w, 0, sizeof(float) * 2 * D, stream);
-  if (e == cudaSuccess) e = cudaMemsetAsync(dlambda, 0, sizeof(float), stream);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
   if (!stats_ready) {
     e = launch_prefill_sm100_stats(m.q128, m.k128, m.v128, nullptr, nullptr, B, N, H, D, causal, lambda, lambda_init,
                                    rms_w, eps, mode, o_maps, reinterpret_cast<float*>(stats), L.n_pad, ctl, stream);
@@ -565,9 +599,14 @@ cudaError_t launch_bwd_sm100_d(const BwdTcMaps& m, const void* dy, int B, int N,
   const long long want = (rows + 7) / 8;
   const int grid = static_cast<int>(want < 148 * 16 ? want : 148 * 16);
   const float dcoef = mode == 0 ? -1.0f : (mode == 2 ? 1.0f : 0.0f);
+  // The CTAs' sums lie in dk and dq until the kernels below write those: 1 and 2d
+  // floats a CTA, which has 2d floats there for each of its eight rows.
   bwd_prep_kernel<D><<<grid, 256, 0, stream>>>(o_maps, static_cast<const __nv_bfloat16*>(dy), rms_w, lambda, mode,
-                                               dcoef, lambda_init, eps, B, N, H, L.n_pad, G, stats, dlambda,
-                                               drms_w, debug_status());
+                                               dcoef, lambda_init, eps, B, N, H, L.n_pad, G, stats, dk, dq,
+                                               debug_status());
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  bwd_sums_kernel<D><<<2 * D / 32 + 1, 1024, 0, stream>>>(dk, dq, grid, dlambda, drms_w);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   GradParams prm = {};
