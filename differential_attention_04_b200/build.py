@@ -9,7 +9,8 @@ bounds-checked variant instead (``-DDIFFATTN_DEBUG``, objects in
 global index and tensor-map coordinate, skip an access out of range and
 record DIFFATTN_ERR_BOUNDS in the status word.  ``csrc/marshal.cpp`` becomes the
 Python module ``_marshal`` (g++, against torch's headers), which marshals the
-calls that a server makes every step.
+calls that a server makes every step; where torch or a header is missing the
+library is built all the same.
 """
 from __future__ import annotations
 
@@ -51,25 +52,40 @@ def _needs_build(obj: str, src: str) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def build_marshal(force: bool = False) -> str:
-    """The marshalling module, in-tree; its torch symbols are those of the torch that imports it."""
+def build_marshal(force: bool = False) -> str | None:
+    """The marshalling module, in-tree; its torch symbols are those of the torch that imports it.
+
+    None where it cannot be built (the library needs neither torch nor Python): the binding then marshals every
+    call itself, and a module of older sources is taken away."""
     src, header = os.path.join(CSRC, "marshal.cpp"), os.path.join(INCLUDE, "diffattn.h")
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
-    newest = max(os.path.getmtime(f) for f in (src, header, os.path.join(torch_dir, "version.py")))
-    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= newest:
+    spec = importlib.util.find_spec("torch")
+    torch_dir = os.path.dirname(spec.origin) if spec and spec.origin else None
+    needed = [src, header] + ([os.path.join(torch_dir, "version.py")] if torch_dir else [])
+    if not force and os.path.exists(MARSHAL) and \
+            all(os.path.exists(f) and os.path.getmtime(f) <= os.path.getmtime(MARSHAL) for f in needed):
         return MARSHAL
-    cuda = os.path.dirname(os.path.dirname(_nvcc()))
-    tmp = MARSHAL + ".tmp"
-    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", src, "-o", tmp, "-I", INCLUDE,
-           "-isystem", os.path.join(torch_dir, "include"), "-isystem", os.path.join(cuda, "include"),
-           "-isystem", sysconfig.get_paths()["include"], "-L", os.path.join(torch_dir, "lib"),
-           "-lc10", "-ltorch_cpu", "-ltorch_python", "-lc10_cuda"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
+    python_h, cxx = sysconfig.get_paths()["include"], shutil.which("g++")
+    missing = [what for what, there in (
+        ("torch with CUDA", torch_dir and os.path.exists(os.path.join(torch_dir, "lib", "libc10_cuda.so"))),
+        ("torch's headers", torch_dir and os.path.isdir(os.path.join(torch_dir, "include"))),
+        ("Python's headers", os.path.exists(os.path.join(python_h, "Python.h"))), ("g++", cxx)) if not there]
+    if not missing:
+        cuda = os.path.dirname(os.path.dirname(_nvcc()))
+        tmp = MARSHAL + ".tmp"
+        cmd = [cxx, "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall", src, "-o", tmp, "-I", INCLUDE,
+               "-isystem", os.path.join(torch_dir, "include"), "-isystem", os.path.join(cuda, "include"),
+               "-isystem", python_h, "-L", os.path.join(torch_dir, "lib"),
+               "-lc10", "-ltorch_cpu", "-ltorch_python", "-lc10_cuda"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode == 0:
+            os.replace(tmp, MARSHAL)
+            return MARSHAL
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError(f"g++ failed on {src}")
-    os.replace(tmp, MARSHAL)
-    return MARSHAL
+        missing = [f"g++ failed on {src}"]
+    sys.stderr.write(f"the marshalling module was not built ({', '.join(missing)}); the binding does without\n")
+    if os.path.exists(MARSHAL):
+        os.remove(MARSHAL)
+    return None
 
 
 def build(verbose_ptxas: bool = False, force: bool = False, debug: bool = False) -> str:
