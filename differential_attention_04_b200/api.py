@@ -62,18 +62,27 @@ def _dev(*ts: torch.Tensor) -> torch.device:
             raise ValueError(f"all tensors must be on one device (found {dev} and {t.device})")
 
 
+def _getters(c):
+    """(current device's index, raw current stream of a device): torch's own raw getters where it has them (a Stream
+    object and a device context cost more host time than the call itself), else its public ones."""
+    return (getattr(c, "_cuda_getDevice", torch.cuda.current_device),
+            getattr(c, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream))
+
+
+_current_device, _raw_stream = _getters(torch._C)
+
+
 def _launch(name: str, tensors, *args) -> None:
     """Call the C entry point `name` with `args` and the current stream of the
     device that `tensors` (every tensor the call reads or writes) live on, with
     that device current: the library launches on the current device."""
     dev = _dev(*tensors)
     fn = getattr(lib(), name)
-    # the raw getters: a Stream object and a device context cost more host time than the call itself
-    if torch._C._cuda_getDevice() == dev.index:
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if _current_device() == dev.index:
+        status = fn(*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+            status = fn(*args, _raw_stream(dev.index))
     if status != OK:
         raise DiffAttnError(name, status)
 

@@ -1,4 +1,6 @@
 """What the binding of the paged serving calls makes of its arguments, before any CUDA call (no GPU needed)."""
+import types
+
 import pytest
 import torch
 
@@ -47,3 +49,10 @@ def test_numbers_beyond_32_bits_are_refused(name, call, x):
     """(A bound of 2^32 new tokens would otherwise reach the library as 0, and nothing would be computed.)"""
     with pytest.raises(ValueError, match=f"^{name} must fit 32 bits"):
         call(x)
+
+
+def test_binding_has_the_public_getters_to_fall_back_on():
+    raw = types.SimpleNamespace(_cuda_getDevice=object(), _cuda_getCurrentRawStream=object())
+    assert api._getters(raw) == (raw._cuda_getDevice, raw._cuda_getCurrentRawStream)
+    device, stream = api._getters(types.SimpleNamespace())
+    assert device is torch.cuda.current_device and callable(stream)

@@ -74,3 +74,26 @@ def test_extend_without_an_epsilon(d, new, kv, H, G, causal):
         assert bool((out[cu[s]:cu[s] + blind] == 0).all())
         # float32 sums of 2d squares and their rsqrt: below 2^-12
         assert bool(((rows[blind:] / 0.36 - 1).abs() <= 2 * 2.0 ** -8 + 2.0 ** -16 + 2.0 ** -12).all())
+
+
+def test_public_getters_make_the_same_calls(monkeypatch):
+    """The binding on a torch without the raw getters: the current stream and device are still those of the call."""
+    class Bare:
+        pass
+
+    q = torch.randn(64, 4, 2, 128, device=DEV)
+    pos, table = i32(np.arange(64)), api.rope_table(64, 128)
+    want = api.rope(q, None, pos, table)[0]
+    device, stream = api._getters(Bare())
+    monkeypatch.setattr(api, "_current_device", device)
+    monkeypatch.setattr(api, "_raw_stream", stream)
+    side = torch.cuda.Stream()
+    assert stream(0) == torch.cuda.current_stream().cuda_stream
+    with torch.cuda.stream(side):
+        assert stream(0) == side.cuda_stream
+        side.wait_stream(torch.cuda.default_stream())
+        got = torch.zeros_like(q)
+        api._launch("diffattn_rope", (q, pos, table, got), q.data_ptr(), None, pos.data_ptr(), table.data_ptr(), 64, 64, 4,
+                    0, 128, 128, api.F32, 0, 0, got.data_ptr(), None)
+    side.synchronize()
+    assert torch.equal(got, want)
