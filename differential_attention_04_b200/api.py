@@ -23,6 +23,8 @@ F32, BF16 = 0, 1
 MODE_DIFF, MODE_LAMBDA_ZERO, MODE_SUM = 0, 1, 2
 # which channels a rotation pairs: (2j, 2j + 1) or (j, j + rot / 2)
 ROPE_INTERLEAVED, ROPE_HALF = 0, 1
+# added to either: rows that are not rotated are written as zeros instead of being left
+ROPE_PAD_ZERO = 256
 # how a rotary table's frequencies are scaled
 ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
 
@@ -584,10 +586,12 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table
     """Queries and keys rotated at `positions`: (q', k').  q: [..., H, 2, d], k: [..., H_kv, 2, d] or None, float32
     or bfloat16, with one position (int32) per row of the leading dimensions; table: rope_table or
     rope_table_scaled, whose width says how many channels are rotated.  Rows with a negative position are left as
-    they are in `out` (which may be (q, k) itself).  ``inverse`` is the transposed map: gradients with respect to
+    they are in `out` (which may be (q, k) itself), or zeros with ROPE_PAD_ZERO added to `layout`; without `out` they
+    are zeros.  ``inverse`` is the transposed map: gradients with respect to
     q', k' go in, those with respect to q, k come out."""
     if out is None:
         out = (torch.empty_like(q), None if k is None else torch.empty_like(k))
+        layout = int(layout) | ROPE_PAD_ZERO
     _need(len(out) == 2, "out must hold (q', k')")
     fast = marshal()
     if fast and _made("diffattn_rope", fast.rope(q, k, positions, table, layout, 1 if inverse else 0, *out)):
@@ -641,9 +645,12 @@ def kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torc
               layout: int = ROPE_INTERLEAVED, out: torch.Tensor | None = None) -> torch.Tensor:
     """The cache write of a step: returns q rotated at `positions`, and writes k rotated and v into the pages at
     `slots` (int32 [T], page * page_size + offset; negative: nothing is written).  q: bfloat16 [T, H, 2, d];
-    k: [T, H_kv, 2, d]; v: [T, H_kv, 2d]; table None: no rotation."""
+    k: [T, H_kv, 2, d]; v: [T, H_kv, 2d]; table None: no rotation (q is copied whole).  Rows with a negative position
+    write nothing and are left as they are in `out` (which may be q), or zeros with ROPE_PAD_ZERO added to `layout`;
+    without `out` they are zeros."""
     if out is None:
         out = torch.empty_like(q)
+        layout = int(layout) | ROPE_PAD_ZERO
     fast = marshal()
     if fast and _made("diffattn_kv_append",
                       fast.kv_append(q, k, v, positions, slots, table, k_cache, v_cache, layout, out)):

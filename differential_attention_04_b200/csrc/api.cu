@@ -281,6 +281,7 @@ int check_heads(int T, int H, int H_kv, int d) {
 int check_rotation(int T, int H, int H_kv, int d, int rot, int layout, const void* positions, const float* table,
                    int n_pos) {
   if (T < 0 || H < 1 || H_kv < 0 || d < 1 || rot < 2 || rot > d || rot % 2) return DIFFATTN_ERR_INVALID_ARG;
+  layout &= ~DIFFATTN_ROPE_PAD_ZERO;
   if (layout != DIFFATTN_ROPE_INTERLEAVED && layout != DIFFATTN_ROPE_HALF) return DIFFATTN_ERR_INVALID_ARG;
   if (!positions || !table || n_pos < 1) return DIFFATTN_ERR_INVALID_ARG;
   if (!aligned16(table) || !aligned4(positions)) return DIFFATTN_ERR_INVALID_ARG;
@@ -665,8 +666,9 @@ int diffattn_rope(const void* q, const void* k, const int* positions, const floa
   p.d = d;
   p.rot = rot;
   p.inverse = inverse ? 1 : 0;
+  p.pad_zero = layout & DIFFATTN_ROPE_PAD_ZERO;
   if (status_ptr(&p.status) != cudaSuccess) return DIFFATTN_ERR_CUDA;
-  return cuda_status(launch_rope_rows(p, dtype == DIFFATTN_BF16, layout, stream));
+  return cuda_status(launch_rope_rows(p, dtype == DIFFATTN_BF16, layout & ~DIFFATTN_ROPE_PAD_ZERO, stream));
 }
 
 int diffattn_kv_append(const void* q, const void* k, const void* v, const int* positions, const int* slots,
@@ -716,8 +718,9 @@ int diffattn_kv_append(const void* q, const void* k, const void* v, const int* p
   p.d = d;
   p.rot = rot;
   p.num_slots = num_pages * page_size;
+  p.pad_zero = layout & DIFFATTN_ROPE_PAD_ZERO;
   if (status_ptr(&p.status) != cudaSuccess) return DIFFATTN_ERR_CUDA;
-  return cuda_status(launch_rope_rows(p, 1, layout, stream));
+  return cuda_status(launch_rope_rows(p, 1, layout & ~DIFFATTN_ROPE_PAD_ZERO, stream));
 }
 
 int diffattn_paged_step(const int* ctx_lens, const int* new_lens, int S, int* block_table, int max_pages,

@@ -145,6 +145,7 @@ struct RopeParams {
   const int *positions, *slots;
   const float* table;  // [n_pos][rot / 2] (cos, sin); null: no rotation (cache write only)
   int n_pos, T, H, H_kv, d, rot, inverse, num_slots;
+  int pad_zero;  // rows of q and k (not the caches') that are not rotated are written as zeros
   int* status;
 };
 cudaError_t launch_rope_rows(const RopeParams& p, int bf16, int layout, cudaStream_t stream);

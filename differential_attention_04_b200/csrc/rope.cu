@@ -138,10 +138,19 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_rows_kernel(const RopePa
         }
       }
     }
-    if (pos < 0) return;  // a padding row
-    if (p.table && pos >= p.n_pos) {
-      record_bounds(p.status);
-      return;
+    if (pos < 0 || (p.table && pos >= p.n_pos)) {  // a padding row, or one without an angle: left as it is, or zeros
+      if (pos >= 0) record_bounds(p.status);
+      if (!p.pad_zero) return;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = r0 + i * g.lanes;
+        if (r >= rows || (r >= q_rows && p.slots)) continue;  // (a cache's rows are left)
+        T* dst = r < q_rows ? static_cast<T*>(p.q_out) + (static_cast<size_t>(t) * q_rows + r) * p.d
+                            : static_cast<T*>(p.k_out) + (static_cast<size_t>(t) * k_rows + r - q_rows) * p.d;
+        *reinterpret_cast<V*>(dst + c0) = V{};
+        if (has_b) *reinterpret_cast<V*>(dst + c0 + second) = V{};
+      }
+      continue;
     }
     if (p.slots && slot >= p.num_slots) record_bounds(p.status);
     const bool kv_ok = !p.slots || (slot >= 0 && slot < p.num_slots);

@@ -501,7 +501,11 @@ int diffattn_paged_step(const int* ctx_lens, const int* new_lens, int S, int* bl
 /* Which channels form a rotated pair, for rot rotated channels. */
 typedef enum {
   DIFFATTN_ROPE_INTERLEAVED = 0, /* (2j, 2j + 1): the layout of diffattn_qkv_proj */
-  DIFFATTN_ROPE_HALF = 1         /* (j, j + rot / 2)                              */
+  DIFFATTN_ROPE_HALF = 1,        /* (j, j + rot / 2)                              */
+  DIFFATTN_ROPE_PAD_ZERO = 256   /* added to either: rows of q_out and k_out that
+                                    are not rotated (a negative position, or one
+                                    behind the table) are written as zeros instead
+                                    of being left; rows of caches stay as they are */
 } diffattn_rope_layout;
 
 /* How a table's frequencies theta_j = base^(-2j/rot) are scaled by `factor` s
@@ -530,7 +534,7 @@ typedef enum {
  *   q, q_out : [T, H, 2, d], k, k_out : [T, H_kv, 2, d], dtype F32 or BF16; the
  *              outputs may be the inputs (any other overlap is refused); H_kv = 0: no k
  *   positions: device int32[T]; a row with a negative position is padding and
- *              its output is left as it is
+ *              its output is left as it is (or zeros: DIFFATTN_ROPE_PAD_ZERO)
  *   table    : device float32 [n_pos][rot / 2][2], as the table calls write it
  *   rot      : even, 2 <= rot <= d; channels from rot on are copied
  *   inverse  : nonzero -> the transposed map (sin negated).  It takes the
@@ -549,7 +553,9 @@ typedef enum {
  *              every row of q is copied)
  *   slots    : device int32[T]; a row with a negative slot writes no key or
  *              value; one >= num_pages * page_size records
- *              DIFFATTN_ERR_BOUNDS and writes none.  No slot may occur twice.
+ *              DIFFATTN_ERR_BOUNDS and writes none.  Nor does a row that is not
+ *              rotated (a negative position, or one behind the table).  No slot
+ *              may occur twice.
  *              q, k and v may not lie in the caches.
  * Errors of the three: DIFFATTN_ERR_INVALID_ARG, DIFFATTN_ERR_UNSUPPORTED,
  * DIFFATTN_ERR_CUDA.

@@ -97,3 +97,39 @@ def test_public_getters_make_the_same_calls(monkeypatch):
                     0, 128, 128, api.F32, 0, 0, got.data_ptr(), None)
     side.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("d,rot,dtype", [(128, 128, torch.bfloat16), (128, 64, torch.float32), (64, 22, torch.bfloat16),
+                                         (256, 2, torch.float32), (64, 64, torch.bfloat16)])
+@pytest.mark.parametrize("half", [False, True])
+def test_rows_without_a_position_are_zeros_in_a_new_output(d, rot, dtype, half):
+    """Whatever the allocation held before: a padded batch goes on into products where a NaN would not stay alone."""
+    T, H, Hkv, n_pos = 301, 5, 2, 50
+    pos = np.random.default_rng(d).integers(0, n_pos, T)
+    pos[::3], pos[7] = -1, n_pos
+    table, lay = api.rope_table_scaled(n_pos, rot), api.ROPE_HALF if half else api.ROPE_INTERLEAVED
+    g = torch.Generator(device=DEV).manual_seed(rot)
+    q, k, v = (torch.randn(T, h, *s, generator=g, device=DEV).to(dtype) for h, s in ((H, (2, d)), (Hkv, (2, d)), (Hkv, (2 * d,))))
+    live = torch.as_tensor((pos >= 0) & (pos < n_pos))
+    slots = i32(np.arange(T))
+    kc, vc = (torch.full((10, 32, Hkv, *s), 3.0, device=DEV).bfloat16() for s in ((2, d), (2 * d,)))
+
+    def calls(out):
+        res = list(api.rope(q, k, i32(pos), table, lay, out=out and (out[0].clone(), out[1].clone())))
+        if dtype == torch.bfloat16:
+            res.append(api.kv_append(q, k, v, i32(pos), slots, table, kc, vc, lay, out=out and out[0].clone()))
+        return res
+
+    kept = calls((torch.full_like(q, 5.0), torch.full_like(k, 5.0)))
+    for _ in range(4):  # the next allocations of these sizes would get these blocks
+        del [torch.full_like(x, float("nan")) for x in (q, k, q)][:]
+    zeroed = calls(None)
+    for a, b in zip(kept, zeroed):
+        assert torch.equal(a[live], b[live]) and bool((a[~live] == 5).all()) and bool((b[~live] == 0).all())
+    if dtype == torch.bfloat16:  # the caches' rows of padding are left in both
+        rows = kc.view(-1, Hkv, 2, d)[:T]
+        assert bool((rows[~live] == 3).all()) and torch.equal(rows[live], zeroed[1][live])
+    assert api.device_status() == api.ERR_BOUNDS  # (the position behind the table)
+    qo = torch.full_like(q, 5.0)
+    api.rope(q, None, i32(np.where(pos == n_pos, 0, pos)), table, lay | api.ROPE_PAD_ZERO, out=(qo, None))
+    assert bool((qo[::3] == 0).all()) and api.device_status() == api.OK
