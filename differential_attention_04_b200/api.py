@@ -517,7 +517,7 @@ def paged_step(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torc
 
     ctx_lens, new_lens: int32 [S] (new_lens -1: the request is finished); block_table: int32 [S, max_pages],
     updated; free_pages: int32 ring of free pages, updated; pool: int32 [2] (head, count), replaced in place unless
-    pool_out is given; num_tokens: rows of positions and slots (-1 behind the last new token).  info: int32 [4]
+    pool_out is given (in place costs a second launch where the step has more than 512 tokens or 16 requests); num_tokens: rows of positions and slots (-1 behind the last new token).  info: int32 [4]
     (tokens, pages taken, pages returned, 0 or what is wrong; then the step took nothing)."""
     fast = marshal()
     if fast and (out is None or len(out) == 5):
@@ -688,7 +688,8 @@ class ExtendPlan(NamedTuple):
 def extend_plan(cu_q: torch.Tensor, kv_lens: torch.Tensor, num_tokens: int, H: int, H_kv: int, d: int, max_new: int,
                 causal: bool = True, buf: torch.Tensor | None = None) -> ExtendPlan:
     """The schedule of a step's attention, made once and read by every layer.  cu_q: int32 [S + 1]; kv_lens: int32
-    [S]; num_tokens: rows of q; max_new: a host bound of the new tokens of a request."""
+    [S]; num_tokens: rows of q; max_new: a host bound of the new tokens of a request (close ones are better: one that
+    allows more than 16 rows a key head launches the many-row kernel, 4 to 8 us a layer where there is nothing for it)."""
     S = kv_lens.numel()
     _i32("cu_q", cu_q, S + 1)
     _i32("kv_lens", kv_lens, S)
@@ -712,7 +713,10 @@ def diffattn_extend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                     out: torch.Tensor | None = None) -> torch.Tensor:
     """Differential attention of the step's new tokens over the paged cache.  q: bfloat16 [T, H, 2, d]; k_cache:
     [num_pages, page_size, H_kv, 2, d]; v_cache: [num_pages, page_size, H_kv, 2d]; block_table: int32
-    [S, max_pages]; plan: extend_plan's.  Rows behind the last request are left as they are in `out`."""
+    [S, max_pages]; plan: extend_plan's.  Rows behind the last request are left as they are in `out`, and zeros
+    without it.  T * H * 2d must stay below 2^31.  A call of a layer passes `workspace` (extend_workspace_size bytes,
+    shared by the layers) and `out`: without them both are allocated, `out` is filled, and the call takes the longer
+    way through this function."""
     fast = marshal()
     if fast and workspace is not None and out is not None and _made("diffattn_extend", fast.extend(
             q, k_cache, v_cache, block_table, *plan, lam, lambda_init, rms_w, eps, mode, workspace, out)):

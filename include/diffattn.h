@@ -542,7 +542,9 @@ typedef enum {
  *              the inputs; with m = 1 it is also the inverse.
  * Float32 arithmetic, one rounding.  A position >= n_pos records
  * DIFFATTN_ERR_BOUNDS in the device status word and leaves its row.
- * d a multiple of 8 up to 256 (DIFFATTN_ERR_UNSUPPORTED otherwise).
+ * d a multiple of 8 up to 256 (DIFFATTN_ERR_UNSUPPORTED otherwise); T * 2 *
+ * (H + H_kv) * d and n_pos * rot below 2^31 (else DIFFATTN_ERR_INVALID_ARG), in
+ * diffattn_kv_append too, and there num_pages * page_size.
  *
  * diffattn_kv_append -- the cache write of a step: q rotated into q_out, k
  * rotated and v copied into the pages, in one launch.
@@ -589,6 +591,14 @@ int diffattn_kv_append(const void* q, const void* k, const void* v, const int* p
  *                 overlap on the GPU (and graphs that are replayed at the same
  *                 time) must not share one.
  *   o and workspace may not overlap another buffer (o not q).
+ *   T * H * 2d must stay below 2^31 (else DIFFATTN_ERR_INVALID_ARG), as must
+ *                 num_pages * page_size; the caches' bytes may pass 2^32.
+ * Precision: scores, maxima, sums and norms are float32, the result is rounded
+ * once.  The softmax weights enter the product with V rounded to bf16, as in
+ * diffattn_fwd, for requests with more than 8 rows (new tokens times H / H_kv),
+ * and with 16 bits for the others.  Where max_new * H / H_kv is at most 16, all
+ * requests of the step keep 16 bits; so a request of 9 to 16 rows may differ in
+ * its last bits between plans with a close and with a wide max_new.
  * diffattn_extend_plan -- writes the schedule of a step (>=
  *   diffattn_extend_plan_size bytes, 16-byte aligned) from cu_q and kv_lens
  *   (device, as diffattn_paged_step writes them).  max_new is a host bound of
