@@ -547,7 +547,8 @@ def paged_step(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torc
         out = torch.unsafe_split_with_sizes(
             torch.empty(2 * S + 2 * T + 5, dtype=torch.int32, device=ctx_lens.device), (S + 1, S, T, T, 4))
     else:
-        _need(len(out) == 5, "out must hold (cu_q, kv_lens, positions, slots, info)")
+        _need(len(out) == 5 and all(t is not None for t in out),
+              "out must hold (cu_q, kv_lens, positions, slots, info)")
         for name, t, n in zip(("cu_q", "kv_lens", "positions", "slots", "info"), out, (S + 1, S, T, T, 4)):
             _i32(name, t, n)
         ts += tuple(out)

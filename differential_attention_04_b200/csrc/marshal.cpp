@@ -139,6 +139,8 @@ PyObject* paged_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     std::vector<at::Tensor> made;
     const at::Tensor* out[5];
     const bool fresh = x.none(8);
+    for (int i = 9; fresh && i < 13; ++i)
+      if (!x.none(i)) return status(kNotPlain);
     if (fresh) {
       if (!x.ready()) return status(kNotPlain);
       made = at::unsafe_split_with_sizes(at::empty({2 * S + 2 * static_cast<int64_t>(T) + 5}, ctx->options()), sizes);

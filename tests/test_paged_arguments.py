@@ -56,3 +56,11 @@ def test_binding_has_the_public_getters_to_fall_back_on():
     assert api._getters(raw) == (raw._cuda_getDevice, raw._cuda_getCurrentRawStream)
     device, stream = api._getters(types.SimpleNamespace())
     assert device is torch.cuda.current_device and callable(stream)
+
+
+@pytest.mark.parametrize("missing", range(5))
+def test_step_outputs_come_whole_or_not_at_all(missing):
+    out = [_i(3), _i(2), _i(4), _i(4), _i(4)]
+    out[missing] = None
+    with pytest.raises(ValueError, match="out must hold"):
+        api.paged_step(_i(2), _i(2), _i(2, 3), _i(9), _i(2), 16, 4, out=out)

@@ -133,3 +133,16 @@ def test_rows_without_a_position_are_zeros_in_a_new_output(d, rot, dtype, half):
     qo = torch.full_like(q, 5.0)
     api.rope(q, None, i32(np.where(pos == n_pos, 0, pos)), table, lay | api.ROPE_PAD_ZERO, out=(qo, None))
     assert bool((qo[::3] == 0).all()) and api.device_status() == api.OK
+
+
+@pytest.mark.parametrize("missing", range(5))
+def test_step_with_a_missing_output_does_nothing(missing):
+    out = [i32([9] * n) for n in (2, 1, 3, 3, 4)]
+    kept, out[missing] = out[missing], None
+    bt, ring, pool = i32([[-1, -1]]), i32([0, 1]), i32([0, 2])
+    with pytest.raises(ValueError, match="out must hold"):
+        api.paged_step(i32([0]), i32([3]), bt, ring, pool, 16, 3, out=out)
+    assert bt.tolist() == [[-1, -1]] and pool.tolist() == [0, 2]
+    out[missing] = kept
+    assert api.paged_step(i32([0]), i32([3]), bt, ring, pool, 16, 3, out=out)[0] is out[0]
+    assert out[2].tolist() == [0, 1, 2] and pool.tolist() == [1, 1]
