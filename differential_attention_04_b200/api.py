@@ -716,11 +716,16 @@ def diffattn_extend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     [num_pages, page_size, H_kv, 2, d]; v_cache: [num_pages, page_size, H_kv, 2d]; block_table: int32
     [S, max_pages]; plan: extend_plan's.  Rows behind the last request are left as they are in `out`, and zeros
     without it.  T * H * 2d must stay below 2^31.  A call of a layer passes `workspace` (extend_workspace_size bytes,
-    shared by the layers) and `out`: without them both are allocated, `out` is filled, and the call takes the longer
-    way through this function."""
+    shared by the layers) and `out`: without them both are allocated and `out` is filled with zeros."""
+    if out is None or workspace is None:
+        T, H, d = _rows(q)
+        if workspace is None:
+            workspace = torch.empty(max(extend_workspace_size(plan), 16), dtype=torch.uint8, device=q.device)
+        if out is None:
+            out = torch.zeros((T, H, 2 * d), dtype=q.dtype, device=q.device)
     fast = marshal()
-    if fast and workspace is not None and out is not None and _made("diffattn_extend", fast.extend(
-            q, k_cache, v_cache, block_table, *plan, lam, lambda_init, rms_w, eps, mode, workspace, out)):
+    if fast and _made("diffattn_extend", fast.extend(q, k_cache, v_cache, block_table, *plan, lam, lambda_init, rms_w,
+                                                     eps, mode, workspace, out)):
         return out
     T, H, d = _rows(q)
     num_pages, page_size, H_kv = _cache_shapes(k_cache, v_cache, d, q.dtype)
@@ -732,11 +737,7 @@ def diffattn_extend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     mode = _int32("mode", mode)
     _scalar_f32("lam", lam)
     _f32("rms_w", rms_w, 2 * d)
-    if out is None:
-        out = torch.zeros((T, H, 2 * d), dtype=q.dtype, device=q.device)
     _same("out", out, (T, H, 2 * d), q.dtype)
-    if workspace is None:
-        workspace = torch.empty(max(extend_workspace_size(plan), 16), dtype=torch.uint8, device=q.device)
     _launch("diffattn_extend", (q, k_cache, v_cache, block_table, plan.buf, lam, rms_w, workspace, out),
             q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), max_pages, num_pages,
             page_size, plan.buf.data_ptr(), plan.buf.nbytes, S, T, H, H_kv, d, max_new, lam.data_ptr(),

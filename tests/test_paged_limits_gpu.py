@@ -146,3 +146,17 @@ def test_step_with_a_missing_output_does_nothing(missing):
     out[missing] = kept
     assert api.paged_step(i32([0]), i32([3]), bt, ring, pool, 16, 3, out=out)[0] is out[0]
     assert out[2].tolist() == [0, 1, 2] and pool.tolist() == [1, 1]
+
+
+def test_attention_without_buffers_is_marshalled_too(monkeypatch):
+    """The short form makes the buffers and then the same compiled call as the one that is given them."""
+    q, kc, vc = (torch.randn(*s, device=DEV).bfloat16() for s in ((5, 2, 2, 64), (4, 16, 2, 2, 64), (4, 16, 2, 128)))
+    plan = api.extend_plan(i32([0, 3]), i32([40]), 5, 2, 2, 64, 3)
+    ws = torch.empty(api.extend_workspace_size(plan), dtype=torch.uint8, device=DEV)
+    lam, w, bt, made = torch.tensor([0.3], device=DEV), torch.ones(128, device=DEV), i32([[2, 0, 3]]), []
+    real = api._made
+    monkeypatch.setattr(api, "_made", lambda name, status: made.append(status) or real(name, status))
+    outs = [api.diffattn_extend(q, kc, vc, bt, plan, lam, 0.4, w, **k) for k in (
+        dict(), dict(workspace=ws), dict(out=torch.zeros(5, 2, 128, device=DEV).bfloat16()),
+        dict(workspace=ws, out=torch.zeros(5, 2, 128, device=DEV).bfloat16()))]
+    assert made == [0] * 4 and all(torch.equal(o, outs[0]) for o in outs) and bool((outs[0][3:] == 0).all())
