@@ -93,7 +93,11 @@ __host__ __device__ inline long long most_rows(const ExtendShape& n) {
 // Rows of the narrow class.  Two column tiles (9 to 16 rows) are 20% faster
 // than a 128-row tile, but the kernel that has them takes 7 to 10 us longer over
 // the single tokens of a step with chunks (mixed step 48 against 55 us), so they
-// are for steps that need no wide kernel.
+// are for steps that need no wide kernel.  It goes by the bound of new tokens, since
+// the lengths are on the device.  With a wide bound, requests of 10 and of 16 rows
+// over 32 x 2000 tokens and 16 heads take 260 and 262 us in place of 213 and 219 (d
+// 64: 148 and 150 in place of 129 and 133), and 64 single tokens over 2000 take 340
+// in place of 332 (194, 184), for a wide kernel that finds no work.
 __host__ __device__ inline int narrow_rows(const ExtendShape& n) {
   return most_rows(n) > 8 && most_rows(n) <= 16 ? 16 : 8;
 }

@@ -28,16 +28,18 @@
 // owns tensor memory and issues the MMAs, warp 3 copies finished tiles out,
 // warps 4-7 do softmax and epilogue, one query row per thread.  Pipeline and
 // barriers are the prefill's; barrier phases count segments (epi_free), tiles
-// (K, V, S, P) or combined segments (the exchange).
+// (K, V, S, P) or combined segments (the exchange and the hand-over to warp 3).
+// After a wait that ran out the softmax warps leave together at the start of the
+// next epilogue, and every other role at its next wait.
 //
 // Bound: as the prefill, the softmax warps and the serial issue of products
 // (about 2500 cycles a 128-key tile against 1540 of tensor work) for long
 // chunks; memory for few rows over many keys; and about 20 thousand cycles an
 // item for its exchange and refill, which short prompts feel (74 x 128 tokens
 // over 12 heads: 147 us).  Measured: 2048 tokens behind 30K cached ones over 12
-// heads 906 us at full clock (1290 TFLOP/s), 1030 us in a loop under the power
-// cap; 2048 behind 6K 237 us (239 without the pairs of F2).  Two softmax warpgroups with 64 keys each were
-// not faster here (chunk 1285 against 1280 us, mixed step 136 against 132).
+// heads 900 us in single calls with pauses (1300 TFLOP/s), 1030 us in a loop under
+// the power cap; 2048 behind 6K 237 us (239 without the pairs of F2).  Two
+// softmax warpgroups with 64 keys each were not faster here (chunk 1285 against 1280 us, mixed step 136 against 132).
 #include "extend_wide.cuh"
 
 namespace diffattn {

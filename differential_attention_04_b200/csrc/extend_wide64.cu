@@ -8,7 +8,7 @@
 //   S_m = Q_m K_m^T  ->  softmax (warpgroup m)  ->  O_m += P_m V
 // alternate on the tensor cores, one map's products under the other's softmax.
 // (As a cluster of two CTAs with a map each, extend_wide.cu's way, ragged
-// prompts of 8 K tokens over 16 heads took 365 us with all launches, this way 217.)
+// prompts of 8 K tokens over 16 heads took 365 us with all launches, this way 218.)
 //
 // Tensor memory: the scores of map m are taken 64 keys at a time into two
 // buffers, at 128 m and 128 m + 64; O_m (128 columns) is at 256 + 128 m.  P_m

@@ -184,11 +184,11 @@ int diffattn_bwd(const void* q, const void* k, const void* v, const void* dy,
  *   v, dy       : device bf16 [B, N, H, 2d]
  *   other arguments, outputs and layouts as in diffattn_bwd
  *   workspace   : device, >= diffattn_bwd_tc_workspace_size bytes, 16-byte aligned
- * Five stream-ordered launches: the prefill in a statistics mode (per map
+ * Six stream-ordered launches: the prefill in a statistics mode (per map
  * A_i V and the log-sum-exp per row), a per-row pass for dO, dw and dlambda,
- * and one kernel each for dV, dK and dQ.  No allocation.  dlambda and drms_w
- * are summed with atomics (last bits may vary from run to run); dq, dk, dv
- * are deterministic.
+ * the sums of those two (whose parts lie in dk and dq until then), and one
+ * kernel each for dV, dK and dQ.  No allocation.  All five gradients repeat
+ * bit for bit.
  * Errors: DIFFATTN_ERR_INVALID_ARG (null or unaligned pointers, bad mode or
  * sizes), DIFFATTN_ERR_UNSUPPORTED (d other than 64 or 128),
  * DIFFATTN_ERR_WORKSPACE, DIFFATTN_ERR_CUDA; DIFFATTN_ERR_TIMEOUT through
