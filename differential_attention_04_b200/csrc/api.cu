@@ -357,8 +357,8 @@ using namespace diffattn;
 
 extern "C" {
 
-// 1.01: adds diffattn_quantize_qk4 and diffattn_fwd_qk4; 1.02: the paged serving calls
-int diffattn_version(void) { return 102; }
+// 1.01: adds diffattn_quantize_qk4 and diffattn_fwd_qk4; 1.02: the paged serving calls; 1.03: DIFFATTN_ROPE_PAD_ZERO
+int diffattn_version(void) { return 103; }
 
 const char* diffattn_status_string(int s) {
   switch (s) {

@@ -123,8 +123,8 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const int* __
     }
     if (is_wide) v.tiles = (nq + tpt - 1) / tpt;
     const PlanSums at = plan_scan(v, sm, total);
-    if (v.reqs) {
-      const int i = DA_CHECK(status, carry.reqs + at.reqs < n.S) ? carry.reqs + at.reqs : 0;
+    const int i = carry.reqs + at.reqs;
+    if (v.reqs && DA_CHECK(status, i < n.S)) {
       narrow[i] = NarrowReq{q0, nq, L, s};
       npre[i] = carry.units + at.units;
     }

@@ -650,7 +650,8 @@ const char* diffattn_status_string(int status);
 
 /* Library ABI version (major * 100 + minor); 101 adds the 4-bit pair
  * diffattn_quantize_qk4 / diffattn_fwd_qk4 to 100, 102 the paged serving calls
- * (diffattn_paged_step, the rotary calls, diffattn_kv_append, diffattn_extend). */
+ * (diffattn_paged_step, the rotary calls, diffattn_kv_append, diffattn_extend),
+ * 103 DIFFATTN_ROPE_PAD_ZERO. */
 int diffattn_version(void);
 
 #ifdef __cplusplus

@@ -36,3 +36,26 @@ def test_every_gradient_repeats(B, N, H, d):
                                         api.MODE_DIFF, ws)
         assert all(torch.equal(a, b) for a, b in zip(want, got))
     assert api.device_status() == api.OK
+
+
+def test_a_captured_backward_repeats():
+    inp = wl.make_prefill(1, 700, 3, 64, causal=True, dtype="bf16", seed=8, device="cuda")
+    dy = torch.randn_like(inp.v)
+    lam = api.diffattn_lambda(inp.lq1, inp.lk1, inp.lq2, inp.lk2, inp.lambda_init)
+    ws = torch.empty(api.bwd_tc_workspace_size(1, 700, 3, 64), dtype=torch.uint8, device="cuda")
+    f32 = dict(dtype=torch.float32, device="cuda")
+    out = tuple(torch.empty(s, **f32) for s in (inp.q.shape, inp.k.shape, inp.v.shape, 1, 128))
+    run = lambda: api.diffattn_bwd_tc(inp.q, inp.k, inp.v, dy, lam, inp.lambda_init, inp.rms_w, inp.eps, True,
+                                      workspace=ws, out=out)
+    want = [x.clone() for x in run()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(3):
+        for x in out:
+            x.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    del graph

@@ -160,3 +160,43 @@ def test_attention_without_buffers_is_marshalled_too(monkeypatch):
         dict(), dict(workspace=ws), dict(out=torch.zeros(5, 2, 128, device=DEV).bfloat16()),
         dict(workspace=ws, out=torch.zeros(5, 2, 128, device=DEV).bfloat16()))]
     assert made == [0] * 4 and all(torch.equal(o, outs[0]) for o in outs) and bool((outs[0][3:] == 0).all())
+
+
+def test_calls_from_several_threads():
+    """Host threads with a stream and buffers of their own, over one plan and one cache."""
+    import threading
+
+    new, kv, H, Hkv, d, page = [1, 5, 140], [700, 90, 300], 4, 2, 128, 16
+    held = [-(-x // page) for x in kv]
+    table = np.full((3, max(held)), -1)
+    for s, n in enumerate(held):
+        table[s, :n] = np.arange(n) + sum(held[:s])
+    g = torch.Generator(device=DEV).manual_seed(1)
+    bf = lambda *s: torch.randn(*s, generator=g, device=DEV).bfloat16()
+    T = sum(new)
+    q, kc, vc, bt = bf(T, H, 2, d), bf(sum(held), page, Hkv, 2, d), bf(sum(held), page, Hkv, 2 * d), i32(table)
+    lam, w, cos = torch.tensor([0.3], device=DEV), torch.ones(2 * d, device=DEV), api.rope_table(T, d)
+    plan = api.extend_plan(i32(np.concatenate([[0], np.cumsum(new)])), i32(kv), T, H, Hkv, d, max(new))
+    pos = i32(np.arange(T))
+    want = [api.diffattn_extend(q, kc, vc, bt, plan, lam, 0.4, w), api.rope(q, None, pos, cos)[0]]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                ws = torch.empty(api.extend_workspace_size(plan), dtype=torch.uint8, device=DEV)
+                for _ in range(40):
+                    got = [api.diffattn_extend(q, kc, vc, bt, plan, lam, 0.4, w, workspace=ws),
+                           api.rope(q, None, pos, cos)[0]]
+                    if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                        bad.append("a result differs")
+        except Exception as e:  # an assertion in a thread would pass unseen
+            bad.append(repr(e))
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
