@@ -598,7 +598,9 @@ int diffattn_kv_append(const void* q, const void* k, const void* v, const int* p
  * diffattn_fwd, for requests with more than 8 rows (new tokens times H / H_kv),
  * and with 16 bits for the others.  Where max_new * H / H_kv is at most 16, all
  * requests of the step keep 16 bits; so a request of 9 to 16 rows may differ in
- * its last bits between plans with a close and with a wide max_new.
+ * its last bits between plans with a close and with a wide max_new.  Errors are
+ * relative to the two maps' terms: where these nearly cancel (lambda near 1 and
+ * maps alike), their difference keeps fewer bits, with bf16 weights above all.
  * diffattn_extend_plan -- writes the schedule of a step (>=
  *   diffattn_extend_plan_size bytes, 16-byte aligned) from cu_q and kv_lens
  *   (device, as diffattn_paged_step writes them).  max_new is a host bound of
