@@ -588,8 +588,8 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table
     or bfloat16, with one position (int32) per row of the leading dimensions; table: rope_table or
     rope_table_scaled, whose width says how many channels are rotated.  Rows with a negative position are left as
     they are in `out` (which may be (q, k) itself), or zeros with ROPE_PAD_ZERO added to `layout`; without `out` they
-    are zeros.  ``inverse`` is the transposed map: gradients with respect to
-    q', k' go in, those with respect to q, k come out."""
+    are zeros.  ``inverse`` is the transposed map: gradients with respect to q', k' go in, those with respect to q, k
+    come out.  q and k together stay below 2^31 elements, and so does the table."""
     if out is None:
         out = (torch.empty_like(q), None if k is None else torch.empty_like(k))
         layout = int(layout) | ROPE_PAD_ZERO
@@ -648,7 +648,7 @@ def kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torc
     `slots` (int32 [T], page * page_size + offset; negative: nothing is written).  q: bfloat16 [T, H, 2, d];
     k: [T, H_kv, 2, d]; v: [T, H_kv, 2d]; table None: no rotation (q is copied whole).  Rows with a negative position
     write nothing and are left as they are in `out` (which may be q), or zeros with ROPE_PAD_ZERO added to `layout`;
-    without `out` they are zeros."""
+    without `out` they are zeros.  q and k together stay below 2^31 elements, and the cache below 2^31 tokens."""
     if out is None:
         out = torch.empty_like(q)
         layout = int(layout) | ROPE_PAD_ZERO
