@@ -40,7 +40,7 @@
 // drafted tokens where this takes 355 (a lone request of 1000 tokens: 14 and 17
 // us).
 //
-// Measured (d 128), over several GPUs: the 64 requests above 1717 to 1777 us, 6.9
+// Measured (d 128), over several GPUs: the 64 requests above 1717 to 1814 us, 6.8
 // to 7.2 TB/s (12.3 GB); the drafted tokens 335 to 355 us, 6.1 to 6.4 TB/s.
 #include <math.h>
 
